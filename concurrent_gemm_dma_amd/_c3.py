@@ -40,7 +40,17 @@ C3_MAX_MASK_WORDS = 8
 C3_MAX_WORLD = 64
 C3_MAX_CURVE = 16
 C3_NOALLOC_SCRATCH_BYTES = 16 << 20  # c3_gemm_noalloc: fixed split-K partials per device
-C3_ABI_VERSION = 5
+C3_ABI_VERSION = 6
+C3_BF16 = 0
+C3_F32 = 1
+C3_SCORE_SOFTMAX = 0
+C3_SCORE_SIGMOID = 1
+C3_MX4_FLOOR = 0
+C3_MX4_UP = 1
+C3_MX4_PAD = 256
+C3_MAX_EXPERTS = 1024
+C3_MAX_TOP_K = 64
+C3_PLAN_WORKSPACE_BYTES = 2 << 20
 TAXONOMY = {0: "GC-equal", 1: "G-long", 2: "C-long"}
 
 # Every symbol include/c3.h declares.
@@ -48,7 +58,8 @@ EXPORTS = ("c3_init", "c3_finalize", "c3_last_error", "c3_device_info", "c3_stre
            "c3_stream_destroy", "c3_cu_mask_balanced", "c3_probe_placement", "c3_gemm",
            "c3_gemm_noalloc", "c3_probe_mfma_rate",
            "c3_gather", "c3_all2all_block", "c3_reduce_scatter", "c3_allreduce_local",
-           "c3_flush_llc", "c3_run_concurrent", "c3_derive_metrics", "c3_roofline_time",
+           "c3_route", "c3_route_backward", "c3_route_plan", "c3_mx4_bytes", "c3_mx4_quantize",
+           "c3_mx4_dequantize", "c3_mx4_gemm", "c3_mx4_gemm_experts", "c3_flush_llc", "c3_run_concurrent", "c3_derive_metrics", "c3_roofline_time",
            "c3_predict_partition", "c3_hybrid_share")
 
 
@@ -133,6 +144,13 @@ class c3_metrics(ctypes.Structure):
         return d
 
 
+class c3_route_opts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -180,6 +198,18 @@ def load(path: Optional[str] = None):
     L.c3_allreduce_local.argtypes = [vp, vp, ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.c_int,
                                      ctypes.c_int, ctypes.c_size_t, ctypes.c_int,
                                      ctypes.POINTER(c3_move_opts), vp]
+    i64, i32 = ctypes.c_int64, ctypes.c_int
+    L.c3_route.argtypes = [vp, i32, i64, i32, i64, ctypes.POINTER(c3_route_opts), vp, vp, vp, vp]
+    L.c3_route_backward.argtypes = [vp, i32, i64, i32, i64, ctypes.POINTER(c3_route_opts), vp, vp,
+                                    vp, i64, vp]
+    L.c3_route_plan.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+    L.c3_mx4_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t),
+                               ctypes.POINTER(ctypes.c_size_t)]
+    L.c3_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, i32, i32, vp, vp, vp]
+    L.c3_mx4_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    L.c3_mx4_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    L.c3_mx4_gemm_experts.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i64,
+                                      i64, i64, vp]
     L.c3_flush_llc.argtypes = [ctypes.c_size_t, vp]
     L.c3_run_concurrent.argtypes = [ctypes.POINTER(c3_gemm_args), ctypes.POINTER(c3_copy_args),
                                     ctypes.POINTER(c3_conc_opts), ctypes.POINTER(c3_timing)]
@@ -327,6 +357,69 @@ def c3_allreduce_local(dst, reduced, contribs, peers, rank: int, chunk_bytes: in
     check(load().c3_allreduce_local(_ptr(dst), _ptr(reduced), _ptr_array(contribs),
                                     _ptr_array(peers), len(contribs), rank, chunk_bytes, mover, o,
                                     _stream(stream)))
+
+
+def route_opts(score: int = C3_SCORE_SOFTMAX, top_k: int = 1, n_groups: int = 1,
+               top_groups: int = 1, group_top: int = 1, renormalize: bool = True,
+               scale: float = 1.0) -> c3_route_opts:
+    return c3_route_opts(score, top_k, n_groups, top_groups, group_top, int(bool(renormalize)),
+                         scale, 0)
+
+
+def c3_route(logits, dtype: int, n_tokens: int, n_experts: int, ld: int, opts, bias, idx, weights,
+             stream=None) -> None:
+    check(load().c3_route(_ptr(logits), dtype, n_tokens, n_experts, ld, _opts(opts), _ptr(bias),
+                          _ptr(idx), _ptr(weights), _stream(stream)))
+
+
+def c3_route_backward(logits, dtype: int, n_tokens: int, n_experts: int, ld: int, opts, idx,
+                      dweights, dlogits, ld_d: int, stream=None) -> None:
+    check(load().c3_route_backward(_ptr(logits), dtype, n_tokens, n_experts, ld, _opts(opts),
+                                   _ptr(idx), _ptr(dweights), _ptr(dlogits), ld_d,
+                                   _stream(stream)))
+
+
+def c3_route_plan(idx, n_tokens: int, top_k: int, n_experts: int, order, offsets,
+                  stream=None) -> None:
+    check(load().c3_route_plan(_ptr(idx), n_tokens, top_k, n_experts, _ptr(order), _ptr(offsets),
+                               _stream(stream)))
+
+
+def c3_mx4_bytes(rows: int, cols: int) -> tuple:
+    """(bytes of codes, bytes of scales) of an MX FP4 operand of rows x cols."""
+    codes, scales = ctypes.c_size_t(), ctypes.c_size_t()
+    check(load().c3_mx4_bytes(rows, cols, ctypes.byref(codes), ctypes.byref(scales)))
+    return codes.value, scales.value
+
+
+def c3_mx4_quantize(x, dtype: int, rows: int, cols: int, ld: int, transpose: bool, rule: int,
+                    codes, scales, stream=None) -> None:
+    check(load().c3_mx4_quantize(_ptr(x), dtype, rows, cols, ld, int(transpose), rule, _ptr(codes),
+                                 _ptr(scales), _stream(stream)))
+
+
+def c3_mx4_dequantize(codes, scales, rows: int, cols: int, y, dtype: int, ld: int,
+                      stream=None) -> None:
+    check(load().c3_mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(y), dtype, ld,
+                                   _stream(stream)))
+
+
+def c3_mx4_gemm(A, sA, B, sB, C, dtype: int, M: int, N: int, K: int, ldc: int,
+                stream=None) -> None:
+    check(load().c3_mx4_gemm(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C), dtype, M, N, K, ldc,
+                             _stream(stream)))
+
+
+def c3_mx4_gemm_experts(A, sA, a_rows: int, B, sB, order, offsets, weights, C, dtype: int,
+                        n_tokens: int, top_k: int, n_experts: int, N: int, K: int, ldc: int,
+                        stream=None) -> None:
+    check(load().c3_mx4_gemm_experts(_ptr(A), _ptr(sA), a_rows, _ptr(B), _ptr(sB), _ptr(order),
+                                     _ptr(offsets), _ptr(weights), _ptr(C), dtype, n_tokens, top_k,
+                                     n_experts, N, K, ldc, _stream(stream)))
+
+
+def _opts(o):
+    return None if o is None else ctypes.byref(o)
 
 
 def c3_flush_llc(nbytes: int, stream=None) -> None:

@@ -182,16 +182,6 @@ c3_status copy_isolated(const c3_copy_args& a, hipStream_t stream) {
 
 using namespace c3;
 
-#define C3_ENTRY(body)                                                      \
-    try {                                                                   \
-        std::lock_guard<std::recursive_mutex> lock_(api_mutex());           \
-        body                                                                \
-    } catch (const std::exception& e) {                                     \
-        return fail(C3_E_INVALID, "internal exception: %s", e.what());      \
-    } catch (...) {                                                         \
-        return fail(C3_E_INVALID, "internal exception");                    \
-    }
-
 extern "C" {
 
 c3_status c3_init(int hip_device) { C3_ENTRY(return init_device(hip_device);) }

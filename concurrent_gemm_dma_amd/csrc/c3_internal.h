@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <exception>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -43,6 +44,17 @@ void clear_error();
         c3_status st_ = (expr);           \
         if (st_ != C3_OK) return st_;     \
     } while (0)
+
+// Body of an entry point: takes the library mutex and turns C++ exceptions into a status.
+#define C3_ENTRY(body)                                                      \
+    try {                                                                   \
+        std::lock_guard<std::recursive_mutex> lock_(api_mutex());           \
+        body                                                                \
+    } catch (const std::exception& e) {                                     \
+        return fail(C3_E_INVALID, "internal exception: %s", e.what());      \
+    } catch (...) {                                                         \
+        return fail(C3_E_INVALID, "internal exception");                    \
+    }
 
 // ---- library state --------------------------------------------------------------------------
 struct Context {
@@ -131,6 +143,58 @@ struct MoverSplit {
 };
 c3_status split_movers(int mover, const c3_move_opts& o, const std::vector<Segment>& segs,
                        MoverSplit* out);
+
+// ---- expert layers (route.hip, mx4.hip, mx4_gemm.hip; entry points in layer.cpp) -----------------
+struct RouteArgs {
+    const void* logits = nullptr;
+    c3_dtype dtype = C3_F32;
+    int64_t T = 0, ld = 0;
+    int E = 0;
+    c3_route_opts o{};
+    const float* bias = nullptr;
+    int32_t* idx = nullptr;       // forward: written; backward: read
+    float* weights = nullptr;     // forward: written
+    const float* dweights = nullptr;
+    void* dlogits = nullptr;
+    int64_t ld_d = 0;
+};
+c3_status route_enqueue(const RouteArgs& a, hipStream_t stream);
+c3_status route_backward_enqueue(const RouteArgs& a, hipStream_t stream);
+// `workspace`: C3_PLAN_WORKSPACE_BYTES, needed where plan_needs_workspace says so.
+bool plan_needs_workspace(int64_t slots);
+c3_status plan_enqueue(const int32_t* idx, int64_t T, int top_k, int E, int32_t* order,
+                       int32_t* offsets, void* workspace, hipStream_t stream);
+
+constexpr int64_t mx4_padded(int64_t cols) {
+    return (cols + C3_MX4_PAD - 1) / C3_MX4_PAD * C3_MX4_PAD;
+}
+struct Mx4Quant {
+    const void* x = nullptr;  // quantise: read; dequantise: written through y
+    void* y = nullptr;
+    c3_dtype dtype = C3_F32;
+    int64_t rows = 0, cols = 0, ld = 0;  // of the operand; ld of x or y
+    bool transpose = false;              // x holds the operand's transpose
+    bool up = false;
+    uint8_t* codes = nullptr;
+    uint8_t* scales = nullptr;
+};
+c3_status mx4_quantize_enqueue(const Mx4Quant& q, hipStream_t stream);
+c3_status mx4_dequantize_enqueue(const Mx4Quant& q, hipStream_t stream);
+
+struct Mx4Gemm {
+    const uint8_t *A = nullptr, *sA = nullptr, *B = nullptr, *sB = nullptr;
+    void* C = nullptr;
+    c3_dtype dtype = C3_BF16;
+    int M = 0, N = 0, K = 0;  // M: rows of C (experts: all slots)
+    int64_t ldc = 0;
+    // experts (order != nullptr)
+    const int32_t *order = nullptr, *offsets = nullptr;
+    const float* weights = nullptr;
+    int T = 0, top_k = 0, E = 0;
+    int64_t a_rows = 0;
+};
+c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream);
+void layer_release_workspaces();
 
 // ---- SDMA (sdma.cpp) ----------------------------------------------------------------------------
 c3_status sdma_discover();

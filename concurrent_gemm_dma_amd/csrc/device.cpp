@@ -132,6 +132,7 @@ void finalize_device() {
     (void)hipDeviceSynchronize();
     release_streams();
     gemm_release_workspaces();
+    layer_release_workspaces();
     if (c.flush_buf) (void)hipFree(c.flush_buf);
     c.flush_buf = nullptr;
     c.flush_bytes = 0;

@@ -37,7 +37,7 @@
 extern "C" {
 #endif
 
-#define C3_ABI_VERSION 5
+#define C3_ABI_VERSION 6
 #define C3_MAX_MASK_WORDS 8 /* CU masks cover up to 256 CUs, bit i = CU i as the driver numbers it */
 #define C3_MAX_SEGMENTS 4096
 #define C3_MAX_WORLD 64 /* ranks of a reduce-scatter / all-reduce local share */
@@ -357,6 +357,128 @@ c3_status c3_allreduce_local(void* dst, void* reduced, const void* const* contri
  * and leaves it holding clean lines (writes one word per workgroup into the scratch's first
  * 8 KiB). Allocates the scratch on first use or growth; below 32 KiB nothing is done. */
 c3_status c3_flush_llc(size_t bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Expert layers with 4-bit weights: what a GPU computes between the two all-to-alls of an expert
+ * layer. Routing chooses every token's experts and lays the choices out by expert; activations
+ * and weights are held in MX FP4; one call multiplies every expert's rows by its weights.
+ *
+ * Slots: choice j of token t is slot j * T + t (T tokens), so that the rows of one choice are a
+ * contiguous [T][N] block and c3_reduce_scatter over the top_k blocks adds up a token's experts.
+ *
+ * MX FP4 operand of `rows` x `cols`, blocks along cols: with P = cols rounded up to a multiple of
+ * C3_MX4_PAD, codes[rows][P/2] bytes (column 2i in the low nibble of byte i, 2i+1 in the high
+ * one) and scales[rows][P/32] bytes. A code is e2m1: sign, then magnitude 0, 0.5, 1, 1.5, 2, 3, 4
+ * or 6. A block is 32 columns of one row; its scale byte s stands for 2^(s-127), and 255 makes
+ * the whole block NaN. What is past cols is zero in both arrays. codes and scales are 16-byte
+ * aligned; c3_mx4_bytes gives their sizes.
+ *
+ * Every call here is stream-ordered, asynchronous and deterministic (no atomics in any result,
+ * fixed summation order). Buffers a call writes must not overlap those it reads (C3_E_OVERLAP).
+ * ------------------------------------------------------------------------------------------- */
+
+typedef enum { C3_BF16 = 0, C3_F32 = 1 } c3_dtype;
+typedef enum { C3_SCORE_SOFTMAX = 0, C3_SCORE_SIGMOID = 1 } c3_score;
+
+/* The block's exponent, from the largest magnitude a of its 32 values:
+ * FLOOR: floor(log2 a) - 2, so a becomes 4..8 units and what is above 6 saturates;
+ * UP:    one more where a would exceed 6 units, so nothing saturates. */
+typedef enum { C3_MX4_FLOOR = 0, C3_MX4_UP = 1 } c3_mx4_rule;
+
+#define C3_MX4_PAD 256
+#define C3_MAX_EXPERTS 1024
+#define C3_MAX_TOP_K 64
+
+/* How c3_route scores and chooses. */
+typedef struct {
+    int32_t score;       /* c3_score */
+    int32_t top_k;       /* experts per token: 1 .. min(n_experts, C3_MAX_TOP_K) */
+    int32_t n_groups;    /* experts fall into n_groups equal runs (1 = no groups; divides
+                            n_experts; at most 64) */
+    int32_t top_groups;  /* groups a token may choose from: 1 .. n_groups */
+    int32_t group_top;   /* a group is worth its best expert (1), or the sum of its two best (2) */
+    int32_t renormalize; /* 1 = a token's weights are its chosen scores over their sum */
+    float scale;         /* every weight is multiplied by this (finite) */
+    int32_t reserved;
+} c3_route_opts;
+
+/* Choose top_k of n_experts for each of n_tokens. logits[n_tokens][ld] (dtype); bias[n_experts]
+ * fp32 or NULL; idx[n_tokens][top_k] int32 and weights[n_tokens][top_k] fp32 are written.
+ * Scores s: softmax over the token's reachable experts, or sigmoid of each logit. A logit of
+ * -infinity or NaN puts its expert out of the token's reach; +infinity counts as the largest
+ * finite fp32. Experts are chosen by s + bias (by the logits themselves without a bias), best
+ * first, equal ones by the lower index; the bias moves only the choice, never the weights. An
+ * expert whose s + bias is -infinity or NaN is out of reach of the choice.
+ * With n_groups > 1 only experts of the token's top_groups best groups can be chosen: a group's
+ * worth is its best expert's value (group_top = 1) or the sum of s + bias over its two best
+ * (group_top = 2; one if it has one in reach).
+ * Choices are those of exact scores up to the rounding of 64-bit floating point.
+ * weights: the chosen s, over their sum if renormalize (correct also where every s underflows),
+ * times scale. Where fewer than top_k experts are in reach the rest have idx -1 and weight 0.
+ * n_tokens = 0 is a no-op. 1 <= n_experts <= C3_MAX_EXPERTS, ld >= n_experts. */
+c3_status c3_route(const void* logits, c3_dtype dtype, int64_t n_tokens, int n_experts, int64_t ld,
+                   const c3_route_opts* opts, const float* bias, int32_t* idx, float* weights,
+                   void* stream);
+
+/* Gradient of c3_route's weights: dlogits[n_tokens][ld_d] (dtype, rounded once) from
+ * dweights[n_tokens][top_k], with the same logits and options and the idx it returned. The choice
+ * itself has no gradient; out-of-reach experts get 0. Entries of idx outside [0, n_experts)
+ * count as absent. An expert named twice by a token collects both gradients. All of
+ * dlogits[t][0..n_experts) is written. */
+c3_status c3_route_backward(const void* logits, c3_dtype dtype, int64_t n_tokens, int n_experts,
+                            int64_t ld, const c3_route_opts* opts, const int32_t* idx,
+                            const float* dweights, void* dlogits, int64_t ld_d, void* stream);
+
+/* Lay the slots out by expert: order[n_tokens * top_k] lists the slots of expert 0, then those of
+ * expert 1, ...; within an expert by token, then choice; slots without an expert (idx outside
+ * [0, n_experts)) come last. offsets[n_experts + 1]: expert e owns order[offsets[e] ..
+ * offsets[e+1]). n_tokens = 0 gives offsets of 0. n_tokens * top_k < 2^31.
+ * Above 4096 slots the call needs C3_PLAN_WORKSPACE_BYTES of device memory, which the library
+ * allocates per stream on first need (kept until c3_finalize); on a stream that is being
+ * captured into a graph that first need is refused (C3_E_UNSUPPORTED): plan once before. */
+#define C3_PLAN_WORKSPACE_BYTES (2u << 20)
+c3_status c3_route_plan(const int32_t* idx, int64_t n_tokens, int top_k, int n_experts,
+                        int32_t* order, int32_t* offsets, void* stream);
+
+/* Sizes of the two arrays of an MX FP4 operand (host arithmetic only; either pointer may be
+ * NULL). 0 <= rows < 2^31, 1 <= cols < 2^31. */
+c3_status c3_mx4_bytes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Quantise x[rows][ld] (dtype; cols <= ld) to the MX FP4 operand of rows x cols, or with
+ * transpose = 1 to that of its transpose, cols x rows (blocks along x's rows). Codes are rounded
+ * to nearest, ties to even, and saturate at 6; exponents below -127 become -127; a block with an
+ * infinity or NaN gets scale 255 and codes 0. x may have any element alignment.
+ * rows = 0 or cols = 0 is a no-op; both below 2^31. */
+c3_status c3_mx4_quantize(const void* x, c3_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                          int transpose, c3_mx4_rule rule, void* codes, void* scales,
+                          void* stream);
+
+/* The values of an MX FP4 operand of rows x cols: y[rows][ld] (dtype; cols <= ld, any element
+ * alignment; what is past cols in a row is left alone). Exact, but for values past the type's
+ * largest (infinity). */
+c3_status c3_mx4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols,
+                            void* y, c3_dtype dtype, int64_t ld, void* stream);
+
+/* C[M][ldc] = A . B^T for MX FP4 operands A (M x K) and B (N x K), fp32 accumulation, C rounded
+ * once to dtype (N <= ldc, any element alignment; what is past N in a row is left alone).
+ * M = 0 or N = 0 is a no-op; M, N <= 2^21, 1 <= K <= 2^21. */
+c3_status c3_mx4_gemm(const void* A, const void* sA, const void* B, const void* sB, void* C,
+                      c3_dtype dtype, int64_t M, int64_t N, int64_t K, int64_t ldc, void* stream);
+
+/* Every expert's product with the rows routed to it, for the slots of c3_route_plan:
+ *     C[slot][0..N) = weight(slot) * A[row(slot)] . B[expert(slot)]^T,
+ * zeros for slots without an expert. A is an operand of a_rows x K: a_rows = n_tokens (every
+ * choice of token t reads row t) or n_tokens * top_k (slot s reads row s). B is one operand of
+ * (n_experts * N) x K, expert e's N rows starting at row e * N. weights[n_tokens][top_k] fp32
+ * multiplies in fp32 before the one rounding to dtype; NULL = 1. C has n_tokens * top_k rows of
+ * ldc >= N. order and offsets are read on the device only; entries outside their ranges are
+ * skipped, never followed. n_tokens = 0 or N = 0 is a no-op; N, K <= 2^21, n_tokens * top_k <=
+ * 2^24, n_experts <= C3_MAX_EXPERTS; A's codes must stay below 4 GiB (C3_E_UNSUPPORTED). */
+c3_status c3_mx4_gemm_experts(const void* A, const void* sA, int64_t a_rows, const void* B,
+                              const void* sB, const int32_t* order, const int32_t* offsets,
+                              const float* weights, void* C, c3_dtype dtype, int64_t n_tokens,
+                              int top_k, int n_experts, int64_t N, int64_t K, int64_t ldc,
+                              void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Concurrent run (C3)

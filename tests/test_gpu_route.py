@@ -1,0 +1,270 @@
+"""Routing on the GPU against the 64-bit definitions of layer_ref: choices and plans exactly,
+weights and gradients within derived bounds, on masks, ties, infinities and NaN; the three calls
+in a captured graph; refusals that need the device."""
+import numpy as np
+import pytest
+
+import layer_ref as ref
+
+pytestmark = pytest.mark.gpu
+KINDS = {"softmax": 0, "sigmoid": 1}
+
+
+def dev(x):
+    import torch
+
+    return torch.from_numpy(np.ascontiguousarray(x)).to("cuda:0")
+
+
+def held(x, dtype, ld):
+    """x with row stride ld in the type, NaN past the experts."""
+    import torch
+
+    h = np.full((x.shape[0], ld), np.nan, np.float32)
+    h[:, :x.shape[1]] = x
+    return dev(h).to(torch.bfloat16 if dtype == 0 else torch.float32)
+
+
+def run(c3, x, dtype, k, kind="softmax", groups=1, top_groups=1, group_top=1, bias=None, renorm=True, scale=1.0,
+        ld=None):
+    import torch
+
+    T, E = x.shape
+    idx = torch.full((T + 1, k), -9, dtype=torch.int32, device="cuda:0")
+    w = torch.full((T + 1, k), -9.0, device="cuda:0")
+    o = c3.route_opts(KINDS[kind], k, groups, top_groups, group_top, renorm, scale)
+    c3.c3_route(held(x, dtype, ld or E), dtype, T, E, ld or E, o, None if bias is None else dev(bias), idx, w)
+    torch.cuda.synchronize()
+    assert (idx[T] == -9).all().item() and (w[T] == -9).all().item()
+    return idx[:T].cpu().numpy(), w[:T].cpu().numpy()
+
+
+def logits(rng, T, E, dtype, masked=0.0):
+    x = (1.5 * rng.normal(0, 1, (T, E)) + 0.5 * rng.normal(0, 1, E)).astype(np.float32)
+    if dtype == 0:
+        x = ref.bf16_round(x)
+    if masked:
+        x[rng.random((T, E)) < masked] = -np.inf
+        x[rng.random(T) < 0.1] = -np.inf
+    return x
+
+
+def weights_close(x, idx, got, want, scale=1.0):
+    """Half a step of the rounding to fp32, and of each of the few fp32 steps before it: a rounded
+    exponent of size r shifts e^r by r half steps, and sums of non-negative terms add one each."""
+    with np.errstate(invalid="ignore"):
+        l = np.array([ref.clean(r) for r in x])
+        span = np.zeros((len(x), 1))
+        for t in range(len(x)):
+            fin = l[t][l[t] > -np.inf]
+            span[t] = min(fin.max() - fin.min(), 200.0) if len(fin) else 0.0
+    limit = (span + idx.shape[1] + 24) * 2.0 ** -24 * np.abs(want) + 2.0 ** -126
+    bad = ~(np.abs(got - want) <= limit)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
+
+
+CASES = [dict(T=1, E=256, k=8, kind="sigmoid", groups=8, top_groups=4, group_top=2, bias=True),
+         dict(T=1, E=1, k=1), dict(T=3, E=4, k=4, kind="sigmoid"), dict(T=130, E=128, k=8),
+         dict(T=257, E=64, k=6, renorm=False), dict(T=65, E=65, k=3, bias=True, renorm=False),
+         dict(T=100, E=160, k=6, groups=8, top_groups=3), dict(T=100, E=160, k=6, groups=8, top_groups=3, group_top=2),
+         dict(T=100, E=252, k=8, groups=4, top_groups=1, group_top=2, bias=True, kind="softmax"),
+         dict(T=50, E=256, k=8, kind="sigmoid", renorm=False, scale=2.5), dict(T=33, E=384, k=10, bias=True),
+         dict(T=20, E=1024, k=64, kind="sigmoid", bias=True), dict(T=20, E=1000, k=16, groups=8, top_groups=4),
+         dict(T=64, E=64, k=5, groups=64, top_groups=9, group_top=2, kind="sigmoid")]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c.values()))
+def test_route(c3gpu, case, dtype, masked):
+    c = dict(case)
+    T, E, k = c.pop("T"), c.pop("E"), c.pop("k")
+    rng = np.random.default_rng(T + 3 * E + k)
+    x = logits(rng, T, E, dtype, masked)
+    c["bias"] = (0.1 * rng.normal(0, 1, E)).astype(np.float32) if c.get("bias") else None
+    idx, w = run(c3gpu, x, dtype, k, ld=E + T % 3, **c)
+    want_i, want_w = ref.route(x, k, **c)
+    np.testing.assert_array_equal(idx, want_i)
+    weights_close(x, idx, w, want_w)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_ties_and_near_ties(c3gpu, kind, bias):
+    """Equal values go to the lower index, and scores a rounding of fp32 apart are told apart."""
+    rng = np.random.default_rng(2)
+    T, E, k = 200, 96, 8
+    x = np.round(rng.normal(0, 1, (T, E)) * 2).astype(np.float32) / 2  # many equal logits
+    x[::2] += (rng.integers(-3, 4, (T // 2, E)) * 2.0 ** -23).astype(np.float32)  # a few steps apart
+    b = (rng.integers(-2, 3, E) / 8).astype(np.float32) if bias else None
+    for groups, top, gt in ((1, 1, 1), (8, 3, 1), (8, 3, 2)):
+        idx, _ = run(c3gpu, x, 1, k, kind, groups, top, gt, b)
+        want = ref.route(x, k, kind, groups, top, gt, b)[0]
+        np.testing.assert_array_equal(idx, want)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_special_values(c3gpu, kind, renorm):
+    """Tokens without experts, one expert, infinities, NaN, the type's lowest value, scores that
+    underflow and that saturate; a bias of -infinity takes an expert out."""
+    low = float(np.finfo(np.float32).min)
+    x = np.zeros((10, 70), np.float32)
+    x[0] = -np.inf
+    x[1] = np.nan
+    x[2] = -np.inf
+    x[2, 69] = -3
+    x[3, 7], x[3, 8] = np.inf, np.inf
+    x[4, 5] = np.nan
+    x[5] = low
+    x[6] = np.linspace(-300, -200, 70)
+    x[7] = np.linspace(200, 300, 70)
+    x[8] = np.linspace(-80, 80, 70)
+    x[9] = low
+    x[9, 3], x[9, 60] = 1.0, 2.0
+    idx, w = run(c3gpu, x, 1, 4, kind, renorm=renorm)
+    want_i, want_w = ref.route(x, 4, kind, renorm=renorm)
+    np.testing.assert_array_equal(idx, want_i)
+    weights_close(x, idx, w, want_w)
+    assert (idx[:2] == -1).all() and (w[:2] == 0).all() and list(idx[2]) == [69, -1, -1, -1]
+    bias = np.zeros(70, np.float32)
+    bias[:60] = -np.inf
+    idx, w = run(c3gpu, x, 1, 4, kind, bias=bias, renorm=renorm)
+    want_i, want_w = ref.route(x, 4, kind, bias=bias, renorm=renorm)
+    np.testing.assert_array_equal(idx, want_i)
+    weights_close(x, idx, w, want_w)
+
+
+def gradient(c3, x, dtype, idx, dw, kind, renorm, scale, ld=None):
+    import torch
+
+    T, E = x.shape
+    out = torch.full((T + 1, ld or E), -9.0, dtype=torch.bfloat16 if dtype == 0 else torch.float32, device="cuda:0")
+    o = c3.route_opts(KINDS[kind], idx.shape[1], renormalize=renorm, scale=scale)
+    c3.c3_route_backward(held(x, dtype, ld or E), dtype, T, E, ld or E, o, dev(idx), dev(dw), out, ld or E)
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    assert (got[T] == -9).all() and (got[:, E:] == -9).all()
+    return got[:T, :E]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (5, 8, 8), (130, 64, 6), (67, 200, 3), (33, 256, 8), (9, 1000, 40)])
+def test_route_backward(c3gpu, T, E, k, kind, renorm, dtype):
+    rng = np.random.default_rng(T + E)
+    x = logits(rng, T, E, dtype, 0.2 if T > 5 else 0.0)
+    idx, _ = ref.route(x, k, kind)
+    if T > 30:
+        idx[3], idx[4, 1], idx[5, 0] = -1, E, -7   # absent entries of every sort
+        idx[6, 1] = idx[6, 0]                      # an expert named twice
+        idx[7, 0] = int(np.argmin(np.where(np.isneginf(x[7]), -1e30, x[7])))  # maybe out of reach
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32)
+    got = gradient(c3gpu, x, dtype, idx, dw, kind, renorm, 1.5, ld=E + 3)
+    want, size = ref.route_gradient(x, idx, dw, kind, renorm, 1.5)
+    half = 2.0 ** -8 if dtype == 0 else 2.0 ** -24
+    # exponents of size below 40 and sums of up to E terms, each rounded in fp32
+    limit = (40 + 24 + k + E / 8) * 2.0 ** -24 * size + half * np.abs(want) + 2.0 ** -126
+    bad = ~(np.abs(got - want) <= limit)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_against_differences(c3gpu, kind, renorm):
+    """dlogits . v is the slope of the forward's weights along v."""
+    rng = np.random.default_rng(11)
+    T, E, k, h = 40, 32, 4, 2.0 ** -7
+    x = rng.normal(0, 1, (T, E)).astype(np.float32)
+    x[np.arange(T)[:, None], np.argsort(rng.random((T, E)), 1)[:, :k]] += 3  # the choice holds along v
+    v = rng.choice([-1.0, 1.0], (T, E)).astype(np.float32)
+    idx, _ = run(c3gpu, x, 1, k, kind, renorm=renorm)
+    up_i, up = run(c3gpu, x + np.float32(h) * v, 1, k, kind, renorm=renorm)
+    dn_i, dn = run(c3gpu, x - np.float32(h) * v, 1, k, kind, renorm=renorm)
+    dw = rng.normal(0, 1, (T, k)).astype(np.float32)
+    d = gradient(c3gpu, x, 1, idx, dw, kind, renorm, 1.0)
+    same = (np.sort(up_i, 1) == np.sort(idx, 1)).all(1) & (np.sort(dn_i, 1) == np.sort(idx, 1)).all(1)
+    assert same.sum() > T // 2
+    for t in np.flatnonzero(same):
+        f = [sum(dw[t, j] * w[t, list(i[t]).index(idx[t, j])] for j in range(k)) for i, w in ((up_i, up), (dn_i, dn))]
+        # truncation h^2 / 6 times a third derivative of at most 8 per weight, rounding 32 half
+        # steps of the weights over 2 h
+        limit = np.abs(dw[t]).sum() * (h * h * 8 / 6 + 64 * 2.0 ** -24 / (2 * h))
+        assert abs((f[0] - f[1]) / (2 * h) - (d[t] * v[t]).sum()) <= limit
+
+
+@pytest.mark.parametrize("T,E,k", [(0, 5, 2), (1, 256, 8), (7, 3, 2), (511, 8, 8), (513, 1024, 8), (700, 24, 6),
+                                   (5000, 1, 1), (9001, 256, 8), (30000, 128, 4), (70001, 1000, 3)])
+def test_plan(c3gpu, T, E, k):
+    import torch
+
+    rng = np.random.default_rng(T)
+    idx = np.minimum((E * rng.random((T, k)) ** 3).astype(np.int32), E - 1)  # uneven
+    idx[rng.random((T, k)) < 0.1] = -1
+    if T > 2:
+        idx[0, 0], idx[2, 0] = E, 1 << 30
+    order = torch.full((T * k + 1,), -9, dtype=torch.int32, device="cuda:0")
+    offsets = torch.full((E + 2,), -9, dtype=torch.int32, device="cuda:0")
+    c3gpu.c3_route_plan(dev(idx), T, k, E, order, offsets)
+    torch.cuda.synchronize()
+    want = ref.plan(idx, E)
+    np.testing.assert_array_equal(order.cpu().numpy(), np.append(want[0], -9))
+    np.testing.assert_array_equal(offsets.cpu().numpy(), np.append(want[1], -9))
+
+
+def test_route_in_a_captured_graph(c3gpu):
+    """Routing, plan, quantisation, experts' products and the gradient recorded once and replayed
+    on new inputs, with eager work between; each replay equals the eager calls bit for bit."""
+    import torch
+
+    c3, T, E, k, N, K = c3gpu, 1100, 16, 4, 200, 320
+    g = torch.Generator(device="cuda:0").manual_seed(1)
+    make = lambda *s: torch.randn(*s, generator=g, device="cuda:0")  # noqa: E731
+    x, logit, dw = make(T, K), make(T, E), make(T, k)
+    o = c3.route_opts(c3.C3_SCORE_SIGMOID, k)
+    empty = lambda n, t=torch.uint8: torch.zeros(n, dtype=t, device="cuda:0")  # noqa: E731
+    b, sb = empty(c3.c3_mx4_bytes(E * N, K)[0]), empty(c3.c3_mx4_bytes(E * N, K)[1])
+    c3.c3_mx4_quantize(make(E * N, K), 1, E * N, K, K, False, 0, b, sb)
+
+    def buffers():
+        nc, ns = c3.c3_mx4_bytes(T, K)
+        return dict(a=empty(nc), sa=empty(ns), idx=empty(T * k, torch.int32), w=empty(T * k, torch.float32),
+                    order=empty(T * k, torch.int32), offsets=empty(E + 1, torch.int32),
+                    C=empty(T * k * N, torch.float32), d=empty(T * E, torch.float32))
+
+    def step(m, s):
+        c3.c3_route(logit, 1, T, E, E, o, None, m["idx"], m["w"], s)
+        c3.c3_route_plan(m["idx"], T, k, E, m["order"], m["offsets"], s)
+        c3.c3_mx4_quantize(x, 1, T, K, K, False, 0, m["a"], m["sa"], s)
+        c3.c3_mx4_gemm_experts(m["a"], m["sa"], T, b, sb, m["order"], m["offsets"], m["w"], m["C"], 1, T, k, E, N, K,
+                               N, s)
+        c3.c3_route_backward(logit, 1, T, E, E, o, m["idx"], dw, m["d"], E, s)
+
+    held, eager = buffers(), buffers()
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(c3.C3Error) as e:  # the plan's workspace cannot be allocated while capturing
+        with torch.cuda.graph(graph, stream=stream):
+            c3.c3_route_plan(held["idx"], T, k, E, held["order"], held["offsets"], stream)
+    assert e.value.status == c3.C3_E_UNSUPPORTED
+    torch.cuda.synchronize()
+    step(held, stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step(held, stream)
+    for i in range(3):
+        logit.copy_(make(T, E))
+        x.copy_(make(T, K))
+        dw.copy_(make(T, k))
+        for t in held.values():
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        step(eager, None)
+        torch.cuda.synchronize()
+        for n in held:
+            assert torch.equal(held[n], eager[n]), (i, n)
