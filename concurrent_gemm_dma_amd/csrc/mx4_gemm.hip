@@ -10,11 +10,18 @@
 // since operands are padded with zeros to a multiple of 256.
 #include "c3_internal.h"
 
+#include <cmath>
+#include <cstdlib>
+#include <type_traits>
+
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 // What the kernels read (one struct argument).
 struct Args {
@@ -74,6 +81,22 @@ __device__ __forceinline__ bool find_rows(const Args& g, int t, Rows& r) {
     return false;
 }
 
+// All tiles of BM positions of the order, the slots without an expert among them; no more than
+// the grid was made for, whatever the offsets hold.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const Args& g) {
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+    for (int e = lane; e <= g.E; e += 64) {
+        const int lo = min(max(g.offsets[e], 0), g.M);
+        const int hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.M) : g.M;
+        n += (hi - lo + BM - 1) / BM;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+    return min(__builtin_amdgcn_readfirstlane(n), g.M / BM + min(g.E + 1, g.M));
+}
+
 // Row of A and of C, and the weight, of one position (slot -1: not a slot; nothing is stored).
 __device__ __forceinline__ int slot_at(const Args& g, int pos, int end) {
     if (pos >= end) return -1;
@@ -90,41 +113,459 @@ __device__ __forceinline__ float weight_of(const Args& g, int slot) {
     return g.weights[(size_t)(slot % g.T) * g.top_k + slot / g.T];
 }
 
+// ------------------------------------------------------------------------------------------------
+// Few rows
+// ------------------------------------------------------------------------------------------------
+// A workgroup computes 16*MT rows x 16*NT columns of C; its waves (4 to 16) take the 512-column
+// chunks of K in turn and add their partial sums up through LDS in wave order, so K is split over
+// a workgroup without a workspace. Operands go straight to registers: in a chunk, lane l reads 64
+// contiguous bytes of row l % 16 (the four blocks 4 * (l / 16) ..), which are its operands of four
+// matrix instructions, and their four scale bytes as one word. B is read once (non-temporal).
+template <int I>
+using Int = std::integral_constant<int, I>;
+
+template <bool STREAM>
+__device__ __forceinline__ i32x4_t load_piece(const uint8_t* p) {
+    const i32x4_t* q = reinterpret_cast<const i32x4_t*>(p);
+    return STREAM ? __builtin_nontemporal_load(q) : *q;
+}
+
+template <int BYTE>
 __device__ __forceinline__ f32x4_t mfma16(i32x4_t a, i32x4_t b, f32x4_t c, int sa, int sb) {
     const i32x8_t x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
     const i32x8_t y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BYTE, sa, BYTE, sb);
 }
 
-// One wave computes 16 rows x 16 columns of C.
-__global__ __launch_bounds__(64) void mx4_gemm_wave16(const Args g) {
+template <int MT, int NT>
+__global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const Args g) {
+    constexpr int BM = 16 * MT, BN = 16 * NT, TILE = BM * BN;
+    extern __shared__ float sums[];  // [waves][BM][BN]
+    __shared__ int slots[BM];
+    __shared__ float factors[BM];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+    const int tiles_n = (g.N + BN - 1) / BN;
     Rows r;
-    const int tiles_n = (g.N + 15) / 16;
-    if (!find_rows<16>(g, blockIdx.x / tiles_n, r)) return;
-    const int lane = threadIdx.x, i = lane & 15, q = lane >> 4;
-    const int n0 = (blockIdx.x % tiles_n) * 16;
-    const int slot = slot_at(g, r.begin + i, r.end);
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    if (r.expert < g.E) {
-        const size_t a = (size_t)row_of(g, slot), b = (size_t)r.expert * g.N + min(n0 + i, g.N - 1);
-        const uint8_t* pa = g.A + a * (g.P / 2) + q * 16;
-        const uint8_t* pb = g.B + b * (g.P / 2) + q * 16;
-        const uint8_t* ps = g.sA + a * (g.P / 32) + q;
-        const uint8_t* pt = g.sB + b * (g.P / 32) + q;
-        for (int k = 0; k < g.P / 128; ++k)
-            acc = mfma16(*reinterpret_cast<const i32x4_t*>(pb + k * 64),
-                         *reinterpret_cast<const i32x4_t*>(pa + k * 64), acc, pt[k * 4], ps[k * 4]);
+    if (!find_rows<BM>(g, blockIdx.x / tiles_n, r)) return;
+    const int n0 = (blockIdx.x % tiles_n) * BN;
+    if (tid < BM) {
+        const int slot = slot_at(g, r.begin + tid, r.end);
+        slots[tid] = slot;
+        factors[tid] = weight_of(g, slot);
     }
-    if (slot < 0) return;
-    const float w = weight_of(g, slot);
+    f32x4_t acc[MT][NT];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        const int n = n0 + 4 * q + v;
-        if (n >= g.N) break;
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = f32x4_t{};
+    if (r.expert < g.E) {
+        const size_t code_row = g.P / 2, scale_row = g.P / 32;
+        const uint8_t *pa[MT], *qa[MT], *pb[NT], *qb[NT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int pos = min(r.begin + m * 16 + i, r.end - 1);
+            const size_t row = (size_t)row_of(g, slot_at(g, pos, r.end));
+            pa[m] = g.A + row * code_row + q * 64;
+            qa[m] = g.sA + row * scale_row + q * 4;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const size_t row = (size_t)r.expert * g.N + min(n0 + n * 16 + i, g.N - 1);
+            pb[n] = g.B + row * code_row + q * 64;
+            qb[n] = g.sB + row * scale_row + q * 4;
+        }
+        // U chunks at once, all of their loads before the first use
+        auto chunks = [&](int c0, bool in, auto u_c) {
+            constexpr int U = decltype(u_c)::value;
+            i32x4_t a[U][MT][4], b[U][NT][4];
+            int sa[U][MT], sb[U][NT];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * waves;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        b[u][n][j] = in ? load_piece<MT == 1>(pb[n] + (size_t)c * 256 + j * 16) : i32x4_t{};
+                    sb[u][n] = in ? *reinterpret_cast<const int*>(qb[n] + c * 16) : 0;
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        a[u][m][j] = in ? load_piece<false>(pa[m] + (size_t)c * 256 + j * 16) : i32x4_t{};
+                    sa[u][m] = in ? *reinterpret_cast<const int*>(qa[m] + c * 16) : 0;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        acc[m][n] = mfma16<0>(b[u][n][0], a[u][m][0], acc[m][n], sb[u][n], sa[u][m]);
+                        acc[m][n] = mfma16<1>(b[u][n][1], a[u][m][1], acc[m][n], sb[u][n], sa[u][m]);
+                        acc[m][n] = mfma16<2>(b[u][n][2], a[u][m][2], acc[m][n], sb[u][n], sa[u][m]);
+                        acc[m][n] = mfma16<3>(b[u][n][3], a[u][m][3], acc[m][n], sb[u][n], sa[u][m]);
+                    }
+        };
+        const int whole = g.P / 512;
+        constexpr int U = MT * NT == 1 ? 4 : 1;
+        int c = wave;
+        for (; c + (U - 1) * waves < whole; c += U * waves) chunks(c, true, Int<U>{});
+        for (; U > 1 && c < whole; c += waves) chunks(c, true, Int<1>{});
+        // the last chunk may have 256 columns only: its upper lanes read nothing
+        if ((g.P & 511) && whole % waves == wave) chunks(whole, q < 2, Int<1>{});
+    }
+    // lane holds columns 16 n + 4 q + v of row 16 m + i
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<f32x4_t*>(&sums[wave * TILE + (m * 16 + i) * BN + n * 16 + 4 * q]) = acc[m][n];
+    __syncthreads();
+    for (int e = tid; e < TILE; e += blockDim.x) {
+        const int m = e / BN, n = n0 + e % BN, slot = slots[m];
+        if (slot < 0 || n >= g.N) continue;
+        float y = sums[e];
+        for (int w = 1; w < waves; ++w) y += sums[w * TILE + e];
+        y = r.expert < g.E ? y * factors[m] : 0.f;
         const size_t o = (size_t)slot * g.ldc + n;
-        const float y = r.expert < g.E ? w * acc[v] : 0.f;
         if (g.f32) static_cast<float*>(g.C)[o] = y;
         else static_cast<__bf16*>(g.C)[o] = static_cast<__bf16>(y);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Tile kernel
+// ------------------------------------------------------------------------------------------------
+// 4 waves (2 x 2), each 32*TM x 32*TN of C from v_mfma_scale_f32_32x32x64_f8f6f4 (lane l: row
+// l % 32, the block l / 32 of a 64-column slice, one scale byte). K goes in stages of 128 columns
+// (64 bytes of a row), four of them in LDS, filled by LDS-direct loads three stages ahead; scales
+// go in slabs of 1024 columns (32 bytes of a row: 64-byte requests would be wasted on less), two
+// of them in LDS. Half h of a wave takes the blocks 2h and 2h + 1 of a stage, so that slice j of
+// the stage is chunk 2h + j of its row.
+//
+// A stage is two slices of TM*TN matrix instructions. While those of one slice run, the wave reads
+// the next slice's fragments, and in the first of the two issues the loads of the stage three
+// ahead (its buffer's last reader finished before the previous stage's barrier). Everything is
+// slotted between matrix instructions by hand, since at TM = TN = 4 one wave per SIMD has nobody
+// to cover for it.
+//
+// The scales of two stages (8 bytes of a row) are read at once and permuted so that the byte of
+// slice j of stage s % 2 is byte 2 * (s % 2) + j of the lane's register, which the instruction
+// selects at no cost.
+//
+// No load leaves its array: rows past M or N are clamped to a valid row, stages past the last one
+// load the last one again into a buffer nobody reads, and a scale unit (16 bytes) that would pass
+// the row's end starts 8 bytes earlier instead (its one pair of stages is then read 8 bytes later).
+#define C3_LDS __attribute__((address_space(3)))
+#define C3_WAIT_VMCNT(n) \
+    __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
+
+__device__ __forceinline__ i32x4_t rsrc_of(const void* base) {
+    const uint64_t a = (uint64_t)(uintptr_t)base;
+    i32x4_t w;
+    w.x = (int)(uint32_t)a;
+    w.y = (int)((uint32_t)(a >> 32) & 0xFFFFu);
+    w.z = -1;           // every offset is in range by construction
+    w.w = 0x00020000;   // raw buffer, 32-bit data format
+    return w;
+}
+
+// One LDS-direct 16-byte load per lane: lane t's 16 bytes from voff + soff land at lds + 16 * t.
+// Inline asm, so that the compiler's wait insertion leaves it alone: the kernel waits on the
+// vector-memory counter itself before a barrier that precedes every read.
+__device__ __forceinline__ void lds_load(i32x4_t r, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, %3 offen lds"
+        :
+        : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+        : "memory", "m0");
+}
+
+// 16-byte chunk swizzle of 64-byte rows: chunk ^= 2*(r2^r3) + (r1^r2) (r_i = bit i of the row),
+// so that 8 or 16 lanes reading 16 bytes from consecutive rows hit distinct banks.
+__device__ __forceinline__ int swizzle(int row) {
+    const int b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1;
+    return ((b2 ^ b3) << 1) | (b1 ^ b2);
+}
+
+template <int BYTE>
+__device__ __forceinline__ f32x16_t mfma32(i32x4_t a, i32x4_t b, f32x16_t c, int sa, int sb) {
+    const i32x8_t x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+    const i32x8_t y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, BYTE, sa, BYTE, sb);
+}
+
+// Between a wave's LDS writes and its own reads of them: LDS operations of a wave are done in
+// order, so only the compiler has to keep it.
+__device__ __forceinline__ void own_lds_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Workgroup -> tile. Workgroups of one residue mod 8 share an XCD: each residue gets a contiguous
+// range of tiles, walked in groups of 4 tile rows so that the tiles resident at one time on an XCD
+// share rows of A and B in its L2.
+__device__ __forceinline__ void map_tile(int bid, int n, int tiles_m, int tiles_n, int& tm, int& tn) {
+    int logical = bid;
+    if (n >= 8) {
+        const int q = n >> 3, rem = n & 7, x = bid & 7;
+        logical = x * q + (x < rem ? x : rem) + (bid >> 3);
+    }
+    const int per_group = 4 * tiles_n;
+    const int group = logical / per_group, first = group * 4;
+    const int rows = min(tiles_m - first, 4);
+    const int in_group = logical - group * per_group;
+    tm = first + in_group % rows;
+    tn = in_group / rows;
+}
+
+template <int TM, int TN>
+__global__ __launch_bounds__(256, TM * TN == 16 ? 1 : 2) void mx4_gemm_tile(const Args g) {
+    constexpr int BM = 64 * TM, BN = 64 * TN, ROWS = BM + BN;
+    constexpr int STAGE = ROWS * 64, SCALES = 4 * STAGE, SLAB = ROWS * 32, UNIT = ROWS * 16;
+    constexpr int NM = TM * TN, NF = TM + TN;  // matrix instructions of a slice, fragments
+    constexpr int NS = (TM + TN) / 4;          // 64-row groups of scales a wave loads
+    constexpr int LOADS = TM + TN;             // code loads of a wave and stage
+    __shared__ __attribute__((aligned(1024))) char smem[SCALES + 2 * SLAB];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int tiles_n = (g.N + BN - 1) / BN;
+    const int tiles_m = g.order ? count_tiles<BM>(g) : (g.M + BM - 1) / BM;
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+    int tm, tn;
+    map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+    Rows r;
+    if (!find_rows<BM>(g, tm, r)) return;
+    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
+    r.end = __builtin_amdgcn_readfirstlane(r.end);
+    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
+    const int n0 = tn * BN;
+    const int half = lane >> 5, row32 = lane & 31;
+
+    f32x16_t acc[TM][TN];
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni) acc[mi][ni] = f32x16_t{};
+
+    if (r.expert < g.E) {
+        const uint32_t code_row = (uint32_t)g.P / 2, scale_row = (uint32_t)g.P / 32;
+        const uint32_t nk = (uint32_t)g.P / 128, pairs = nk / 2;
+        const size_t a_base = g.order ? 0 : (size_t)r.begin;  // a gather starts at A itself
+        const size_t b_base = (size_t)r.expert * g.N + n0;
+        const i32x4_t rA = rsrc_of(g.A + a_base * code_row), rB = rsrc_of(g.B + b_base * code_row);
+        const i32x4_t rsA = rsrc_of(g.sA + a_base * scale_row), rsB = rsrc_of(g.sB + b_base * scale_row);
+        auto a_row = [&](int i) -> uint32_t {
+            const int pos = min(r.begin + i, r.end - 1);
+            return g.order ? (uint32_t)row_of(g, slot_at(g, pos, r.end)) : (uint32_t)(pos - r.begin);
+        };
+        auto b_row = [&](int i) -> uint32_t { return (uint32_t)min(i, g.N - 1 - n0); };
+
+        // block i of wave w: rows 16 * (T * w + i) + lane / 4, chunk lane % 4
+        uint32_t va[TM], vb[TN], vs[NS];
+        const int q = lane >> 2;
+        const uint32_t chunk = (uint32_t)((lane & 3) ^ swizzle(q)) * 16u;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) va[i] = a_row(16 * (TM * wave + i) + q) * code_row + chunk;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) vb[i] = b_row(16 * (TN * wave + i) + q) * code_row + chunk;
+        bool s_is_a[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int first = 64 * (wave + 4 * i);
+            s_is_a[i] = first < BM;
+            vs[i] = (s_is_a[i] ? a_row(first + lane) : b_row(first - BM + lane)) * scale_row;
+        }
+        const uint32_t lds0 = (uint32_t)(uintptr_t)(C3_LDS char*)smem;
+        auto load_codes = [&](uint32_t k, int st, int i) {  // load i of stage k into buffer st
+            const uint32_t soff = min(k, nk - 1) * 64u;
+            const uint32_t at = lds0 + (uint32_t)(st * STAGE);
+            if (i < TM) lds_load(rA, at + (uint32_t)((TM * wave + i) * 1024), va[i < TM ? i : 0], soff);
+            else lds_load(rB, at + (uint32_t)(BM * 64 + (TN * wave + i - TM) * 1024), vb[i < TM ? 0 : i - TM], soff);
+        };
+        auto load_scales = [&](uint32_t slab, int buf) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t soff = min(slab * 32u + 16u * u, scale_row - 16u);
+                    const uint32_t at = lds0 + (uint32_t)(SCALES + u * UNIT + (wave + 4 * i) * 1024) +
+                                        (uint32_t)buf * SLAB;
+                    lds_load(s_is_a[i] ? rsA : rsB, at, vs[i], soff);
+                }
+        };
+
+        // fragment reads: f < TM of A, then of B
+        const char* lds = smem;
+        uint32_t f_at[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            f_at[j] = (uint32_t)row32 * 64u + (uint32_t)(((2 * half + j) ^ swizzle(row32)) << 4);
+        const uint32_t fa = (uint32_t)(wm * 32 * TM) * 64u, fb = (uint32_t)(BM + wn * 32 * TN) * 64u;
+        i32x4_t frag[2][NF];
+        auto read_frag = [&](int st, int j, int f) {
+            const uint32_t at = (uint32_t)(st * STAGE) + (f < TM ? fa + f * 2048u : fb + (f - TM) * 2048u) + f_at[j];
+            frag[j][f] = *reinterpret_cast<const C3_LDS i32x4_t*>((const C3_LDS char*)lds + at);
+        };
+        const uint32_t sel = half ? 0x07060302u : 0x05040100u;
+        const uint32_t sfa = (uint32_t)(SCALES + (wm * 32 * TM + row32) * 16);
+        const uint32_t sfb = (uint32_t)(SCALES + (BM + wn * 32 * TN + row32) * 16);
+        i32x2_t raw[NF];
+        int sc[2][NF];
+        auto read_scale = [&](uint32_t at, int f) {
+            const uint32_t o = at + (f < TM ? sfa + f * 512u : sfb + (f - TM) * 512u);
+            raw[f] = *reinterpret_cast<const C3_LDS i32x2_t*>((const C3_LDS char*)lds + o);
+        };
+        auto permute = [&](int set, int f) {
+            sc[set][f] = (int)__builtin_amdgcn_perm((uint32_t)raw[f].y, (uint32_t)raw[f].x, sel);
+        };
+        // where the scales of pair p are, in the slab buffers
+        auto pair_at = [&](uint32_t p) -> uint32_t {
+            return ((p >> 2) & 1) * SLAB + ((p >> 1) & 1) * UNIT + ((p & 1) | (p == pairs - 1)) * 8u;
+        };
+
+        // One stage. st: its buffer; PAR: kt % 2; SET: the scales' register set; AHEAD: loads that
+        // may still be in flight when stage kt + 1 has to have landed; SLABS: issue the next slab.
+        auto step = [&](uint32_t kt, int st, auto par_c, auto set_c, auto ahead_c, auto slabs_c) {
+            constexpr int PAR = decltype(par_c)::value, SET = decltype(set_c)::value;
+            constexpr int AHEAD = decltype(ahead_c)::value;
+            constexpr bool SLABS = decltype(slabs_c)::value != 0;
+            const uint32_t next_pair = pair_at((kt + 1) >> 1);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
+                acc[mi][ni] = mfma32<2 * PAR>(frag[0][TM + ni], frag[0][mi], acc[mi][ni], sc[SET][TM + ni], sc[SET][mi]);
+                if (i < NF) read_frag(st, 1, i);
+                if (NM == 4) load_codes(kt + 3, (st + 3) & 3, i);
+                else if (i >= NM - LOADS) load_codes(kt + 3, (st + 3) & 3, i - (NM - LOADS));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (SLABS) load_scales((kt >> 3) + 1, (int)(((kt >> 3) + 1) & 1));
+            C3_WAIT_VMCNT(AHEAD);
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
+                acc[mi][ni] = mfma32<2 * PAR + 1>(frag[1][TM + ni], frag[1][mi], acc[mi][ni], sc[SET][TM + ni],
+                                                  sc[SET][mi]);
+                if (i < NF) {
+                    if (PAR) read_scale(next_pair, i);
+                    read_frag((st + 1) & 3, 0, i);
+                }
+                if (PAR && NM == 16 && i >= 8) permute(SET ^ 1, i - 8);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (PAR && NM != 16)
+#pragma unroll
+                for (int f = 0; f < NF; ++f) permute(SET ^ 1, f);
+        };
+
+        load_scales(0, 0);
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load_codes(s, s, i);
+        C3_WAIT_VMCNT(2 * LOADS);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            read_scale(pair_at(0), f);
+            read_frag(0, 0, f);
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f) permute(0, f);
+
+        // The next slab's loads go out in step 1 of eight, after those of stage 4: they are among
+        // the loads in flight at steps 1 (just issued) and 2.
+        constexpr int L2 = 2 * LOADS, LS = 2 * LOADS + 2 * NS;
+        uint32_t kt = 0;
+        for (; kt + 8 <= nk; kt += 8) {
+            step(kt, 0, Int<0>{}, Int<0>{}, Int<L2>{}, Int<0>{});
+            step(kt + 1, 1, Int<1>{}, Int<0>{}, Int<LS>{}, Int<1>{});
+            step(kt + 2, 2, Int<0>{}, Int<1>{}, Int<LS>{}, Int<0>{});
+            step(kt + 3, 3, Int<1>{}, Int<1>{}, Int<L2>{}, Int<0>{});
+            step(kt + 4, 0, Int<0>{}, Int<0>{}, Int<L2>{}, Int<0>{});
+            step(kt + 5, 1, Int<1>{}, Int<0>{}, Int<L2>{}, Int<0>{});
+            step(kt + 6, 2, Int<0>{}, Int<1>{}, Int<L2>{}, Int<0>{});
+            step(kt + 7, 3, Int<1>{}, Int<1>{}, Int<L2>{}, Int<0>{});
+        }
+        for (; kt < nk; kt += 2) {
+            step(kt, (int)(kt & 3), Int<0>{}, Int<0>{}, Int<L2>{}, Int<0>{});
+            step(kt + 1, (int)((kt + 1) & 3), Int<1>{}, Int<0>{}, Int<L2>{}, Int<0>{});
+#pragma unroll
+            for (int f = 0; f < NF; ++f) sc[0][f] = sc[1][f];
+        }
+        C3_WAIT_VMCNT(0);  // loads past the end still write LDS
+    }
+    __syncthreads();
+
+    // ---- C: 32 rows at a time through LDS (this wave's own 17 KiB), so that it leaves in whole
+    // 128-byte lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each
+    // 32 x 32 block; a row's 16-byte chunks are permuted by its number against bank conflicts.
+    const int size = g.f32 ? 4 : 2;
+    const int row_bytes = 32 * TN * size, chunks = row_bytes / 16;
+    char* out = smem + wave * (32 * 32 * TN * 4 + 32 * 4);
+    int* slots = reinterpret_cast<int*>(out + 32 * 32 * TN * 4);
+    const bool aligned = (((uintptr_t)g.C | (uint64_t)g.ldc * size) & 15) == 0;
+    const int nw = n0 + wn * 32 * TN;
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi) {
+        const int slot = slot_at(g, r.begin + wm * 32 * TM + mi * 32 + row32, r.end);
+        const float w = weight_of(g, slot);
+        if (half == 0) slots[row32] = slot;
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+            for (int v = 0; v < 16; v += 4) {
+                const int n = 32 * ni + 2 * v + 4 * half;
+                f32x4_t y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = r.expert < g.E ? w * acc[mi][ni][v + i] : 0.f;
+                if (g.f32) {
+                    const int c = (n / 4) ^ (row32 & (chunks - 1));
+                    *reinterpret_cast<f32x4_t*>(out + row32 * row_bytes + c * 16) = y;
+                } else {
+                    const int c = (n / 8) ^ (row32 & (chunks - 1));
+                    bf16x4_t b = {static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
+                                  static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
+                    *reinterpret_cast<bf16x4_t*>(out + row32 * row_bytes + c * 16 + (n & 4) * 2) = b;
+                }
+            }
+        own_lds_fence();
+        for (int i = lane; i < 32 * chunks; i += 64) {
+            const int m = i / chunks, c = i % chunks, s = slots[m];
+            const int n = nw + c * (16 / size);
+            if (s < 0 || n >= g.N) continue;
+            const i32x4_t v = *reinterpret_cast<const i32x4_t*>(out + m * row_bytes + (c ^ (m & (chunks - 1))) * 16);
+            char* p = static_cast<char*>(g.C) + ((size_t)s * g.ldc + n) * size;
+            const int fit = (g.N - n) * size;
+            if (fit >= 16 && aligned) {
+                *reinterpret_cast<i32x4_t*>(p) = v;
+            } else if (fit >= 16) {
+                __builtin_memcpy(__builtin_assume_aligned(p, 2), &v, 16);
+            } else if (g.f32) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e * 4 < fit) reinterpret_cast<int*>(p)[e] = v[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e * 2 < fit) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+            }
+        }
+        own_lds_fence();
     }
 }
 
@@ -132,6 +573,35 @@ __global__ __launch_bounds__(64) void mx4_gemm_wave16(const Args g) {
 int64_t most_tiles(const c3::Mx4Gemm& g, int bm) {
     if (!g.order) return (g.M + bm - 1) / bm;
     return g.M / bm + std::min<int64_t>(g.E + 1, g.M);
+}
+
+// Rows of the tile to use: 16, 32, 64 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile).
+int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
+    const double rows = g.order ? (double)g.M / std::min(g.E, g.M) : g.M;  // of an expert, on average
+    if (rows <= 16) return 16;
+    if (rows <= 32) return 32;
+    if (rows <= 64 || P < 512) return 64;
+    auto tiles = [&](int bm) {
+        const double m = g.order ? (double)g.M / bm + 0.5 * std::min(g.E, g.M) : (g.M + bm - 1) / bm;
+        return m * ((g.N + bm - 1) / bm);
+    };
+    const double nk = P / 128;
+    const double t256 = std::ceil(tiles(256) / n_cu) * (18.0 + 0.9 * nk);
+    const double t128 = std::ceil(tiles(128) / (2 * n_cu)) * (10.0 + 0.7 * nk);
+    return t256 < t128 ? 256 : 128;
+}
+
+template <int MT, int NT>
+c3_status launch_rows(const c3::Mx4Gemm& g, const Args& a, int n_cu, hipStream_t stream) {
+    const int64_t groups = most_tiles(g, 16 * MT) * ((g.N + 16 * NT - 1) / (16 * NT));
+    if (groups >= (1 << 22)) return c3::fail(C3_E_INVALID, "MX FP4 product: too many tiles");
+    // as many waves as there are chunks of K, up to what fills the device
+    int waves = 4;
+    while (waves < (MT * NT == 4 ? 16 : 8) && waves * groups < 16 * (int64_t)n_cu && waves * 512 < a.P)
+        waves *= 2;
+    hipLaunchKernelGGL((mx4_gemm_rows<MT, NT>), dim3((unsigned)groups), dim3(64 * waves),
+                       waves * 256 * MT * NT * sizeof(float), stream, a);
+    return C3_OK;
 }
 
 }  // namespace
@@ -142,9 +612,24 @@ c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream) {
     const Args a = {g.A, g.sA, g.B, g.sB, g.C, g.order, g.offsets, g.weights, g.ldc,
                     g.M, g.N, (int)mx4_padded(g.K), g.T, g.top_k, g.order ? g.E : 1,
                     (int)g.a_rows, (int)(g.dtype == C3_F32)};
-    const int64_t groups = (int64_t)((g.N + 15) / 16) * most_tiles(g, 16);
-    if (groups >= (1 << 26)) return fail(C3_E_INVALID, "MX FP4 product: too many tiles");
-    hipLaunchKernelGGL(mx4_gemm_wave16, dim3((unsigned)groups), dim3(64), 0, stream, a);
+    const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
+    int tile = choose_tile(g, a.P, n_cu);
+    const char* force = std::getenv("C3_MX4_TILE");  // tests: every kernel on every shape it can take
+    if (force && *force && (std::atoi(force) <= 64 || a.P >= 512)) tile = std::atoi(force);
+    if (tile >= 128) {
+        const int64_t groups = most_tiles(g, tile) * ((g.N + tile - 1) / tile);
+        if (groups >= (1 << 24)) return fail(C3_E_INVALID, "MX FP4 product: too many tiles");
+        if (tile == 256)
+            hipLaunchKernelGGL((mx4_gemm_tile<4, 4>), dim3((unsigned)groups), dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((mx4_gemm_tile<2, 2>), dim3((unsigned)groups), dim3(256), 0, stream, a);
+    } else if (tile == 16) {
+        C3_TRY((launch_rows<1, 1>(g, a, n_cu, stream)));
+    } else if (tile == 32) {
+        C3_TRY((launch_rows<2, 2>(g, a, n_cu, stream)));
+    } else {
+        C3_TRY((launch_rows<4, 4>(g, a, n_cu, stream)));
+    }
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;
 }
