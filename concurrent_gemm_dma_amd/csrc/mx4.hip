@@ -3,17 +3,20 @@
 // A block is 32 values along the operand's columns: E = floor(log2 max|x|) - 2 (one more by the
 // rule UP where max|x| > 6 * 2^E), at least -127; codes are x / 2^E rounded to e2m1, ties to even,
 // saturating at 6. All of it is exact in fp32: the exponent comes from the bits of max|x|, and
-// x / 2^E is a power-of-two scaling.
+// x / 2^E is a power-of-two scaling, which the conversion instructions apply themselves.
+//
+// All kernels are bound by memory: x (or the values) once, 17/32 bytes a value of codes and scales.
 #include "c3_internal.h"
+
+#include <type_traits>
 
 namespace {
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float load_f32(const void* x, bool bf16, size_t i) {
-    if (!bf16) return static_cast<const float*>(x)[i];
-    return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(x)[i] << 16);
-}
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // Scale byte of a block from the bits of its largest magnitude; 255 for infinity and NaN. With
 // exponent field F, floor(log2 max) - 2 + 127 = F - 2; subnormals (F = 0) clamp to 0 as well.
@@ -23,90 +26,336 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, bool up) {
     return (uint32_t)max(F - 2 + (int)(up && (amax & 0x7FFFFFu) > 0x400000u), 0);
 }
 
-// e2m1 code of x / 2^(byte - 127): thresholds halfway between neighbours, ties to the even code.
-__device__ __forceinline__ uint32_t code_of(float x, uint32_t byte) {
-    const float y = ldexpf(x, 127 - (int)byte);
-    const float a = fabsf(y);
+// e2m1 code of x / 2^-127, for blocks of scale byte 0, whose factor is no normal fp32: thresholds
+// halfway between neighbours, ties to the even code.
+__device__ __noinline__ uint32_t tiny_code(float x) {
+    const float a = fabsf(ldexpf(x, 127));
     const uint32_t c = (uint32_t)(a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) +
                        (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
     return c | ((__builtin_bit_cast(uint32_t, x) >> 28) & 8u);
 }
 
-// One lane quantises one block.
-__global__ __launch_bounds__(256) void quantize_blocks(const void* __restrict__ x, int bf16,
-                                                       int64_t rows, int64_t cols, int64_t ld,
-                                                       int transpose, int up,
-                                                       uint8_t* __restrict__ codes,
-                                                       uint8_t* __restrict__ scales,
-                                                       int64_t blocks_per_row) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * blocks_per_row) return;
-    const int64_t r = i / blocks_per_row, c0 = (i - r * blocks_per_row) * 32;
-    float v[32];
-    uint32_t amax = 0;
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+
+// Eight values in the type they come in: fp32 in eight words, bf16 in four.
+template <bool BF16>
+struct Eight {
+    uint32_t w[BF16 ? 4 : 8];
+};
+
+// Bits of the largest magnitude, as fp32.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest(const Eight<BF16>& x) {
+    if constexpr (BF16) {
+        u16x2_t m = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const int64_t c = c0 + j;
-        v[j] = c < cols ? load_f32(x, bf16, transpose ? (size_t)(c * ld + r) : (size_t)(r * ld + c))
-                        : 0.f;
-        amax = max(amax, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, x.w[i] & 0x7FFF7FFFu));
+        return (uint32_t)max(m.x, m.y) << 16;
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, x.w[i] & 0x7FFFFFFFu);
+        return m;
     }
-    const uint32_t byte = scale_byte(amax, up);
-    u32x4_t out = {0, 0, 0, 0};
-    if (byte != 255u)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) out[j / 8] |= code_of(v[j], byte) << (4 * (j % 8));
-    reinterpret_cast<u32x4_t*>(codes)[i] = out;
-    scales[i] = (uint8_t)byte;
 }
 
-// One lane writes eight values.
-__global__ __launch_bounds__(256) void dequantize_pieces(const uint8_t* __restrict__ codes,
-                                                         const uint8_t* __restrict__ scales,
-                                                         int64_t rows, int64_t cols, int64_t ld,
-                                                         void* __restrict__ y, int bf16,
-                                                         int64_t padded) {
-    const int64_t per_row = (cols + 7) / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * per_row) return;
-    const int64_t r = i / per_row, c0 = (i - r * per_row) * 8;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * (padded / 2) + c0 / 2);
-    const int s = scales[r * (padded / 32) + c0 / 32];
+// The codes of eight values of a block with this scale byte, the first in the low nibble.
+template <bool BF16>
+__device__ __forceinline__ uint32_t encode(const Eight<BF16>& x, uint32_t byte) {
+    if (byte == 0) {
+        uint32_t c = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if (c0 + j >= cols) break;
-        const uint32_t c = (w >> (4 * j)) & 15u;
-        const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-        const float a = e ? ldexpf(1.f + 0.5f * m, (int)e - 1) : 0.5f * m;
-        float v = ldexpf(c & 8u ? -a : a, s - 127);
-        if (s == 255) v = __builtin_nanf("");
-        const size_t o = (size_t)(r * ld + c0 + j);
-        if (bf16) static_cast<__bf16*>(y)[o] = static_cast<__bf16>(v);
-        else static_cast<float*>(y)[o] = v;
+        for (int i = 0; i < 8; ++i) {
+            float v;
+            if constexpr (BF16) v = i & 1 ? bf16_hi(x.w[i / 2]) : bf16_lo(x.w[i / 2]);
+            else v = __builtin_bit_cast(float, x.w[i]);
+            c |= tiny_code(v) << (4 * i);
+        }
+        return c;
+    }
+    const float s = __builtin_bit_cast(float, byte << 23);
+    uint32_t c = 0;
+    if constexpr (BF16) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, x.w[0]), s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, x.w[1]), s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, x.w[2]), s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2_t, x.w[3]), s, 3);
+    } else {
+        auto f = [&](int i) { return __builtin_bit_cast(float, x.w[i]); };
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(0), f(1), s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(2), f(3), s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(4), f(5), s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(6), f(7), s, 3);
+    }
+    return byte == 255u ? 0u : c;
+}
+
+// Eight values at p, of which `fit` belong to the row (the rest are zero). Whole pieces are two
+// or one 16-byte loads whatever the alignment; x is read once (non-temporal).
+template <bool BF16>
+__device__ __forceinline__ Eight<BF16> load_eight(const char* p, int64_t fit) {
+    typedef u32x4_t loose __attribute__((aligned(2)));
+    Eight<BF16> x;
+    if (fit >= 8) {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+            const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const loose*>(p) + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x.w[4 * i + j] = v[j];
+        }
+    } else if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = 2 * i < fit ? reinterpret_cast<const uint16_t*>(p)[2 * i] : 0;
+            const uint32_t hi = 2 * i + 1 < fit ? reinterpret_cast<const uint16_t*>(p)[2 * i + 1] : 0;
+            x.w[i] = lo | hi << 16;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.w[i] = i < fit ? reinterpret_cast<const uint32_t*>(p)[i] : 0;
+    }
+    return x;
+}
+
+// Row and piece of a lane: lane `tid` of a workgroup that starts at piece `first` (counted over
+// all rows of `per_row` pieces). The division is the workgroup's; a lane's part is below
+// per_row + 1024, where multiplying by ceil(2^32 / per_row) is exact up to 2^11 pieces a row, and
+// past that a row ends at most once.
+struct At {
+    int64_t row;
+    uint32_t piece;
+};
+__device__ __forceinline__ At locate(int64_t first, uint32_t tid, uint32_t per_row, uint32_t magic) {
+    const int64_t row = first / per_row;
+    const uint32_t x = (uint32_t)(first - row * per_row) + tid;
+    const uint32_t q = per_row > 2048 ? (uint32_t)(x >= per_row) : __umulhi(x, magic);
+    return {row + q, x - q * per_row};
+}
+constexpr int kThreads = 256;
+constexpr int kPieces = 2;  // of a lane, 256 lanes apart
+
+// Four lanes quantise a block, eight values each.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void quantize_rows(const char* __restrict__ x, int64_t rows,
+                                                          int64_t cols, int64_t ld, int up,
+                                                          uint32_t* __restrict__ codes,
+                                                          uint8_t* __restrict__ scales,
+                                                          uint32_t per_row, uint32_t magic) {
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kPieces);
+    Eight<BF16> v[kPieces];
+    At at[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        at[k] = locate(first, threadIdx.x + k * kThreads, per_row, magic);
+        const int64_t c = (int64_t)at[k].piece * 8;
+        const int64_t fit = at[k].row < rows ? cols - c : 0;
+        v[k] = load_eight<BF16>(x + (at[k].row * ld + c) * (BF16 ? 2 : 4), fit);
+    }
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        uint32_t m = largest<BF16>(v[k]);
+        m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));  // lane ^ 1
+        m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));  // lane ^ 2
+        if (at[k].row >= rows) continue;
+        const uint32_t byte = scale_byte(m, up);
+        const int64_t i = at[k].row * per_row + at[k].piece;
+        codes[i] = encode<BF16>(v[k], byte);
+        if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
     }
 }
+
+// The transpose's operand. A workgroup of 8 waves takes 256 rows of x (one padding unit of the
+// operand's columns) x 64 lanes of columns: wave w the block of rows 32 w .., a lane four bytes of
+// columns (two of bf16, one of fp32), so that a wave reads 256 contiguous bytes of each row and a
+// block's 32 values lie in one lane. The codes pass through LDS and leave as 128 contiguous bytes
+// of every operand row.
+template <bool BF16>
+__global__ __launch_bounds__(512) void quantize_transposed(const char* __restrict__ x, int64_t xrows,
+                                                           int64_t xcols, int64_t ld, int up,
+                                                           uint8_t* __restrict__ codes,
+                                                           uint8_t* __restrict__ scales,
+                                                           int64_t padded, uint32_t tiles) {
+    constexpr int C = BF16 ? 2 : 1, TILE = 64 * C;
+    __shared__ u32x4_t out[TILE * 8];
+    __shared__ __attribute__((aligned(16))) uint8_t bytes[TILE * 8];
+    typedef uint32_t loose __attribute__((aligned(2)));
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t r0 = (int64_t)(blockIdx.x / tiles) * 256 + wave * 32;
+    const int64_t c0 = (int64_t)(blockIdx.x % tiles) * TILE;
+    const int64_t c = c0 + lane * C;
+    const int fit = (int)max(int64_t(0), min<int64_t>(C, xcols - c));  // of this lane's columns
+    const char* p = x + (r0 * ld + c) * (BF16 ? 2 : 4);
+    const int64_t step = ld * (BF16 ? 2 : 4);
+    uint32_t w[32];
+    if (r0 + 32 <= xrows && fit == C) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) w[k] = __builtin_nontemporal_load(reinterpret_cast<const loose*>(p + k * step));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            w[k] = 0;
+            if (r0 + k >= xrows || fit == 0) continue;
+            if (fit == C) w[k] = *reinterpret_cast<const loose*>(p + k * step);
+            else w[k] = *reinterpret_cast<const uint16_t*>(p + k * step);
+        }
+    }
+    uint32_t amax[C];
+    if constexpr (BF16) {
+        u16x2_t m = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[k] & 0x7FFF7FFFu));
+        amax[0] = (uint32_t)m.x << 16;
+        amax[1] = (uint32_t)m.y << 16;
+    } else {
+        amax[0] = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) amax[0] = max(amax[0], w[k] & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const uint32_t byte = scale_byte(amax[j], up);
+        u32x4_t v;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            Eight<BF16> e;
+            if constexpr (BF16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // the column's values of two rows
+                    e.w[i] = __builtin_amdgcn_perm(w[8 * q + 2 * i + 1], w[8 * q + 2 * i], j ? 0x07060302u : 0x05040100u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e.w[i] = w[8 * q + i];
+            }
+            v[q] = encode<BF16>(e, byte);
+        }
+        const int row = lane * C + j;  // of the tile's operand rows
+        out[row * 8 + (wave ^ (lane & 7))] = v;
+        bytes[row * 8 + wave] = (uint8_t)byte;
+    }
+    __syncthreads();
+    const int64_t k0 = (int64_t)(blockIdx.x / tiles) * 256;
+    for (int i = threadIdx.x; i < TILE * 8; i += 512) {
+        const int row = i >> 3, b = i & 7;
+        if (c0 + row >= xcols) break;
+        *reinterpret_cast<u32x4_t*>(codes + (c0 + row) * (padded / 2) + k0 / 2 + b * 16) =
+            out[row * 8 + (b ^ ((row / C) & 7))];
+    }
+    if ((int)threadIdx.x < TILE && c0 + threadIdx.x < xcols)
+        *reinterpret_cast<u32x2_t*>(scales + (c0 + threadIdx.x) * (padded / 32) + k0 / 32) =
+            *reinterpret_cast<const u32x2_t*>(&bytes[threadIdx.x * 8]);
+}
+
+// A lane writes eight values.
+template <bool BF16>
+__global__ __launch_bounds__(kThreads) void dequantize_rows(const uint32_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales,
+                                                            int64_t rows, int64_t cols, int64_t ld,
+                                                            char* __restrict__ y, int64_t padded,
+                                                            uint32_t per_row, uint32_t magic) {
+    typedef u32x4_t loose __attribute__((aligned(2)));
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kPieces);
+    uint32_t c[kPieces], s[kPieces];
+    At at[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        at[k] = locate(first, threadIdx.x + k * kThreads, per_row, magic);
+        if (at[k].row >= rows) continue;
+        const int64_t i = at[k].row * (padded / 8) + at[k].piece;
+        c[k] = codes[i];
+        s[k] = scales[i >> 2];
+    }
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        if (at[k].row >= rows) continue;
+        uint32_t v[BF16 ? 4 : 8];
+        // the smallest scale is no normal fp32: 2^-126 of half the values, which e2m1 holds only
+        // in part, so the instruction's result is halved instead (exact)
+        const float f = __builtin_bit_cast(float, s[k] ? s[k] << 23 : 1u << 23);
+        f32x2_t t[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[k], f, 0),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[k], f, 1),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[k], f, 2),
+                        __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[k], f, 3)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (s[k] == 0) t[i] = {t[i].x * 0.5f, t[i].y * 0.5f};
+            if (s[k] == 255) t[i] = {__builtin_nanf(""), __builtin_nanf("")};
+            if constexpr (BF16) {
+                const bf16x2_t b = {static_cast<__bf16>(t[i].x), static_cast<__bf16>(t[i].y)};
+                v[i] = __builtin_bit_cast(uint32_t, b);
+            } else {
+                const u32x2_t b = __builtin_bit_cast(u32x2_t, t[i]);
+                v[2 * i] = b.x;
+                v[2 * i + 1] = b.y;
+            }
+        }
+        const int64_t col = (int64_t)at[k].piece * 8;
+        char* p = y + (at[k].row * ld + col) * (BF16 ? 2 : 4);
+        const int fit = (int)min<int64_t>(8, cols - col);
+        if (fit == 8) {
+#pragma unroll
+            for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+                const u32x4_t o = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+                __builtin_nontemporal_store(o, reinterpret_cast<loose*>(p) + i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i) {
+                if (i >= fit) break;
+                if constexpr (BF16) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+                else reinterpret_cast<uint32_t*>(p)[i] = v[i];
+            }
+        }
+    }
+}
+
+uint32_t magic_of(uint32_t per_row) { return (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row); }
 
 }  // namespace
 
 namespace c3 {
 
+// Workgroups of one launch: the runtime takes below 2^32 threads.
+static c3_status check_groups(const char* who, int64_t groups, int threads) {
+    if (groups >= (int64_t(1) << 32) / threads)
+        return fail(C3_E_INVALID, "%s: too large for one launch", who);
+    return C3_OK;
+}
+
 c3_status mx4_quantize_enqueue(const Mx4Quant& q, hipStream_t stream) {
-    const int64_t per_row = mx4_padded(q.cols) / 32;
-    const int64_t groups = (q.rows * per_row + 255) / 256;
-    if (groups >= (1 << 24)) return fail(C3_E_INVALID, "c3_mx4_quantize: too large for one launch");
-    hipLaunchKernelGGL(quantize_blocks, dim3((unsigned)groups), dim3(256), 0, stream, q.x,
-                       (int)(q.dtype == C3_BF16), q.rows, q.cols, q.ld, (int)q.transpose, (int)q.up,
-                       q.codes, q.scales, per_row);
+    const int64_t padded = mx4_padded(q.cols);
+    const bool bf16 = q.dtype == C3_BF16;
+    const char* x = static_cast<const char*>(q.x);
+    if (q.transpose) {
+        const int tile = bf16 ? 128 : 64;
+        const int64_t tiles = (q.rows + tile - 1) / tile, groups = tiles * (padded / 256);
+        C3_TRY(check_groups("c3_mx4_quantize", groups, 512));
+        auto kernel = bf16 ? quantize_transposed<true> : quantize_transposed<false>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(512), 0, stream, x, q.cols, q.rows,
+                           q.ld, (int)q.up, q.codes, q.scales, padded, (uint32_t)tiles);
+    } else {
+        const uint32_t per_row = (uint32_t)(padded / 8);
+        const int64_t groups = (q.rows * per_row + kThreads * kPieces - 1) / (kThreads * kPieces);
+        C3_TRY(check_groups("c3_mx4_quantize", groups, kThreads));
+        auto kernel = bf16 ? quantize_rows<true> : quantize_rows<false>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, x, q.rows, q.cols,
+                           q.ld, (int)q.up, reinterpret_cast<uint32_t*>(q.codes), q.scales, per_row,
+                           magic_of(per_row));
+    }
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;
 }
 
 c3_status mx4_dequantize_enqueue(const Mx4Quant& q, hipStream_t stream) {
-    const int64_t groups = (q.rows * ((q.cols + 7) / 8) + 255) / 256;
-    if (groups >= (1 << 24)) return fail(C3_E_INVALID, "c3_mx4_dequantize: too large for one launch");
-    hipLaunchKernelGGL(dequantize_pieces, dim3((unsigned)groups), dim3(256), 0, stream, q.codes,
-                       q.scales, q.rows, q.cols, q.ld, q.y, (int)(q.dtype == C3_BF16),
-                       mx4_padded(q.cols));
+    const uint32_t per_row = (uint32_t)((q.cols + 7) / 8);
+    const int64_t groups = (q.rows * per_row + kThreads * kPieces - 1) / (kThreads * kPieces);
+    C3_TRY(check_groups("c3_mx4_dequantize", groups, kThreads));
+    auto kernel = q.dtype == C3_BF16 ? dequantize_rows<true> : dequantize_rows<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream,
+                       reinterpret_cast<const uint32_t*>(q.codes), q.scales, q.rows, q.cols, q.ld,
+                       static_cast<char*>(q.y), mx4_padded(q.cols), per_row, magic_of(per_row));
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;
 }
