@@ -88,6 +88,51 @@ def test_route(c3gpu, case, dtype, masked):
     weights_close(x, idx, w, want_w)
 
 
+# batches of over 2048 tokens take another arrangement of the lanes
+LARGE = [dict(T=2049, E=17, k=3, kind="sigmoid"), dict(T=2051, E=128, k=8), dict(T=2050, E=100, k=16, renorm=False),
+         dict(T=2049, E=256, k=8, kind="sigmoid", groups=8, top_groups=4, group_top=2, bias=True),
+         dict(T=2300, E=252, k=7, groups=7, top_groups=3, group_top=2, kind="sigmoid"),
+         dict(T=2050, E=48, k=2, groups=16, top_groups=5, bias=True),
+         dict(T=2049, E=30, k=4, groups=3, top_groups=2, group_top=2),
+         dict(T=2049, E=256, k=20, groups=2, top_groups=1, bias=True), dict(T=2049, E=320, k=4),
+         dict(T=2049, E=66, k=2, groups=33, top_groups=7, group_top=2, kind="sigmoid", bias=True)]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "-".join(str(v) for v in c.values()))
+def test_route_large_batches(c3gpu, case, dtype):
+    test_route(c3gpu, case, dtype, 0.1)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_large_batch_ties_and_special_values(c3gpu, bias):
+    rng = np.random.default_rng(4)
+    T, E, k = 2100, 96, 8
+    x = np.round(rng.normal(0, 1, (T, E)) * 2).astype(np.float32) / 2
+    x[::3] = rng.choice(np.array([np.inf, -np.inf, np.nan, np.finfo(np.float32).min, 0.0, -0.0, 1e-45, -1e-45, 200.0],
+                                 np.float32), (T // 3, E))
+    b = (rng.integers(-2, 3, E) / 8).astype(np.float32) if bias else None
+    for kind in ("softmax", "sigmoid"):
+        # sums of two scores with a bias can tie up to their last bits: not compared here
+        for groups, top, gt in ((1, 1, 1), (8, 3, 1 if bias else 2)):
+            idx, w = run(c3gpu, x, 1, k, kind, groups, top, gt, b)
+            want_i, want_w = ref.route(x, k, kind, groups, top, gt, b)
+            np.testing.assert_array_equal(idx, want_i)
+            weights_close(x, idx, w, want_w)
+
+
+@pytest.mark.parametrize("E,groups", [(1020, 17), (990, 33), (1023, 3), (1024, 64)])
+def test_route_many_experts_in_groups(c3gpu, E, groups):
+    rng = np.random.default_rng(E)
+    x = logits(rng, 40, E, 1, 0.1)
+    b = (0.1 * rng.normal(0, 1, E)).astype(np.float32)
+    for bias in (None, b):
+        idx, w = run(c3gpu, x, 1, 12, "sigmoid", groups, 2, 2, bias)
+        want_i, want_w = ref.route(x, 12, "sigmoid", groups, 2, 2, bias)
+        np.testing.assert_array_equal(idx, want_i)
+        weights_close(x, idx, w, want_w)
+
+
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 def test_route_ties_and_near_ties(c3gpu, kind, bias):
@@ -268,3 +313,9 @@ def test_route_in_a_captured_graph(c3gpu):
         torch.cuda.synchronize()
         for n in held:
             assert torch.equal(held[n], eager[n]), (i, n)
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 1024, 1), (65, 9, 1), (8, 5, 8), (4096, 300, 1), (4097, 300, 1),
+                                   (262145, 64, 1), (40000, 1024, 8)])
+def test_plan_at_the_borders_of_its_kernels(c3gpu, T, E, k):
+    test_plan(c3gpu, T, E, k)
