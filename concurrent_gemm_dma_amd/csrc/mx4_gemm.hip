@@ -118,9 +118,10 @@ __device__ __forceinline__ float weight_of(const Args& g, int slot) {
 // ------------------------------------------------------------------------------------------------
 // A workgroup computes 16*MT rows x 16*NT columns of C; its waves (4 to 16) take the 512-column
 // chunks of K in turn and add their partial sums up through LDS in wave order, so K is split over
-// a workgroup without a workspace. Operands go straight to registers: in a chunk, lane l reads 64
-// contiguous bytes of row l % 16 (the four blocks 4 * (l / 16) ..), which are its operands of four
-// matrix instructions, and their four scale bytes as one word. B is read once (non-temporal).
+// a workgroup without a workspace. Operands go straight to registers: load j of a chunk takes
+// block 4 * j + l / 16 of row l % 16 (64 contiguous bytes of each row), which is the lane's operand
+// of matrix instruction j; the row's 16 scale bytes come as one load, of which the lane shifts out
+// byte 4 * j + l / 16. B is read once (non-temporal).
 template <int I>
 using Int = std::integral_constant<int, I>;
 
@@ -130,12 +131,23 @@ __device__ __forceinline__ i32x4_t load_piece(const uint8_t* p) {
     return STREAM ? __builtin_nontemporal_load(q) : *q;
 }
 
-template <int BYTE>
 __device__ __forceinline__ f32x4_t mfma16(i32x4_t a, i32x4_t b, f32x4_t c, int sa, int sb) {
     const i32x8_t x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
     const i32x8_t y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BYTE, sa, BYTE, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
 }
+
+// N * 4 scale bytes, on which rows of an odd number of 256-column units are 8-byte aligned only.
+template <int N>
+struct Scales {
+    int w[N];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        typedef int loose __attribute__((ext_vector_type(N), aligned(8)));
+        const loose v = *reinterpret_cast<const loose*>(p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = v[i];
+    }
+};
 
 template <int MT, int NT>
 __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const Args g) {
@@ -166,36 +178,34 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
         for (int m = 0; m < MT; ++m) {
             const int pos = min(r.begin + m * 16 + i, r.end - 1);
             const size_t row = (size_t)row_of(g, slot_at(g, pos, r.end));
-            pa[m] = g.A + row * code_row + q * 64;
-            qa[m] = g.sA + row * scale_row + q * 4;
+            pa[m] = g.A + row * code_row + q * 16;
+            qa[m] = g.sA + row * scale_row;
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const size_t row = (size_t)r.expert * g.N + min(n0 + n * 16 + i, g.N - 1);
-            pb[n] = g.B + row * code_row + q * 64;
-            qb[n] = g.sB + row * scale_row + q * 4;
+            pb[n] = g.B + row * code_row + q * 16;
+            qb[n] = g.sB + row * scale_row;
         }
-        // U chunks at once, all of their loads before the first use
-        auto chunks = [&](int c0, bool in, auto u_c) {
-            constexpr int U = decltype(u_c)::value;
-            i32x4_t a[U][MT][4], b[U][NT][4];
-            int sa[U][MT], sb[U][NT];
+        // J steps of 128 columns each of U chunks at once, all of their loads before the first use
+        auto chunks = [&](int c0, auto u_c, auto j_c) {
+            constexpr int U = decltype(u_c)::value, J = decltype(j_c)::value;
+            i32x4_t a[U][MT][J], b[U][NT][J];
+            Scales<J> sa[U][MT], sb[U][NT];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = c0 + u * waves;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        b[u][n][j] = in ? load_piece<MT == 1>(pb[n] + (size_t)c * 256 + j * 16) : i32x4_t{};
-                    sb[u][n] = in ? *reinterpret_cast<const int*>(qb[n] + c * 16) : 0;
+                    for (int j = 0; j < J; ++j) b[u][n][j] = load_piece<MT == 1>(pb[n] + (size_t)c * 256 + j * 64);
+                    sb[u][n].load(qb[n] + c * 16);
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        a[u][m][j] = in ? load_piece<false>(pa[m] + (size_t)c * 256 + j * 16) : i32x4_t{};
-                    sa[u][m] = in ? *reinterpret_cast<const int*>(qa[m] + c * 16) : 0;
+                    for (int j = 0; j < J; ++j) a[u][m][j] = load_piece<false>(pa[m] + (size_t)c * 256 + j * 64);
+                    sa[u][m].load(qa[m] + c * 16);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -204,20 +214,19 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        acc[m][n] = mfma16<0>(b[u][n][0], a[u][m][0], acc[m][n], sb[u][n], sa[u][m]);
-                        acc[m][n] = mfma16<1>(b[u][n][1], a[u][m][1], acc[m][n], sb[u][n], sa[u][m]);
-                        acc[m][n] = mfma16<2>(b[u][n][2], a[u][m][2], acc[m][n], sb[u][n], sa[u][m]);
-                        acc[m][n] = mfma16<3>(b[u][n][3], a[u][m][3], acc[m][n], sb[u][n], sa[u][m]);
-                    }
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < J; ++j)
+                            acc[m][n] = mfma16(b[u][n][j], a[u][m][j], acc[m][n], sb[u][n].w[j] >> (8 * q),
+                                               sa[u][m].w[j] >> (8 * q));
         };
         const int whole = g.P / 512;
         constexpr int U = MT * NT == 1 ? 4 : 1;
         int c = wave;
-        for (; c + (U - 1) * waves < whole; c += U * waves) chunks(c, true, Int<U>{});
-        for (; U > 1 && c < whole; c += waves) chunks(c, true, Int<1>{});
-        // the last chunk may have 256 columns only: its upper lanes read nothing
-        if ((g.P & 511) && whole % waves == wave) chunks(whole, q < 2, Int<1>{});
+        for (; c + (U - 1) * waves < whole; c += U * waves) chunks(c, Int<U>{}, Int<4>{});
+        for (; U > 1 && c < whole; c += waves) chunks(c, Int<1>{}, Int<4>{});
+        // the last chunk may have 256 columns only
+        if ((g.P & 511) && whole % waves == wave) chunks(whole, Int<1>{}, Int<2>{});
     }
     // lane holds columns 16 n + 4 q + v of row 16 m + i
 #pragma unroll

@@ -92,6 +92,8 @@ def test_route(c3gpu, case, dtype, masked):
 LARGE = [dict(T=2049, E=17, k=3, kind="sigmoid"), dict(T=2051, E=128, k=8), dict(T=2050, E=100, k=16, renorm=False),
          dict(T=2049, E=256, k=8, kind="sigmoid", groups=8, top_groups=4, group_top=2, bias=True),
          dict(T=2300, E=252, k=7, groups=7, top_groups=3, group_top=2, kind="sigmoid"),
+         dict(T=4098, E=256, k=8, kind="sigmoid", groups=8, top_groups=4, group_top=2, bias=True),
+         dict(T=4097, E=250, k=9, bias=True), dict(T=4099, E=205, k=5, groups=5, top_groups=2),
          dict(T=2050, E=48, k=2, groups=16, top_groups=5, bias=True),
          dict(T=2049, E=30, k=4, groups=3, top_groups=2, group_top=2),
          dict(T=2049, E=256, k=20, groups=2, top_groups=1, bias=True), dict(T=2049, E=320, k=4),
