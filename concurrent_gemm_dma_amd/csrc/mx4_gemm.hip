@@ -11,7 +11,6 @@
 #include "c3_internal.h"
 
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 namespace {
@@ -116,7 +115,7 @@ __device__ __forceinline__ float weight_of(const Args& g, int slot) {
 // ------------------------------------------------------------------------------------------------
 // Few rows
 // ------------------------------------------------------------------------------------------------
-// A workgroup computes 16*MT rows x 16*NT columns of C; its waves (4 to 16) take the 512-column
+// A workgroup computes 16*MT rows x 16*NT columns of C; its waves (1 to 16) take the 512-column
 // chunks of K in turn and add their partial sums up through LDS in wave order, so K is split over
 // a workgroup without a workspace. Operands go straight to registers: load j of a chunk takes
 // block 4 * j + l / 16 of row l % 16 (64 contiguous bytes of each row), which is the lane's operand
@@ -187,46 +186,36 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
             pb[n] = g.B + row * code_row + q * 16;
             qb[n] = g.sB + row * scale_row;
         }
-        // J steps of 128 columns each of U chunks at once, all of their loads before the first use
-        auto chunks = [&](int c0, auto u_c, auto j_c) {
-            constexpr int U = decltype(u_c)::value, J = decltype(j_c)::value;
-            i32x4_t a[U][MT][J], b[U][NT][J];
-            Scales<J> sa[U][MT], sb[U][NT];
+        // J steps of 128 columns, all of their loads before the first use
+        auto chunk = [&](int c, auto j_c) {
+            constexpr int J = decltype(j_c)::value;
+            i32x4_t a[MT][J], b[NT][J];
+            Scales<J> sa[MT], sb[NT];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * waves;
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int j = 0; j < J; ++j) b[n][j] = load_piece<MT == 1>(pb[n] + (size_t)c * 256 + j * 64);
+                sb[n].load(qb[n] + c * 16);
+            }
 #pragma unroll
-                    for (int j = 0; j < J; ++j) b[u][n][j] = load_piece<MT == 1>(pb[n] + (size_t)c * 256 + j * 64);
-                    sb[u][n].load(qb[n] + c * 16);
-                }
+            for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                    for (int j = 0; j < J; ++j) a[u][m][j] = load_piece<false>(pa[m] + (size_t)c * 256 + j * 64);
-                    sa[u][m].load(qa[m] + c * 16);
-                }
+                for (int j = 0; j < J; ++j) a[m][j] = load_piece<false>(pa[m] + (size_t)c * 256 + j * 64);
+                sa[m].load(qa[m] + c * 16);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int j = 0; j < J; ++j)
-                            acc[m][n] = mfma16(b[u][n][j], a[u][m][j], acc[m][n], sb[u][n].w[j] >> (8 * q),
-                                               sa[u][m].w[j] >> (8 * q));
+                    for (int j = 0; j < J; ++j)
+                        acc[m][n] = mfma16(b[n][j], a[m][j], acc[m][n], sb[n].w[j] >> (8 * q), sa[m].w[j] >> (8 * q));
         };
         const int whole = g.P / 512;
-        constexpr int U = MT * NT == 1 ? 4 : 1;
-        int c = wave;
-        for (; c + (U - 1) * waves < whole; c += U * waves) chunks(c, Int<U>{}, Int<4>{});
-        for (; U > 1 && c < whole; c += waves) chunks(c, Int<1>{}, Int<4>{});
+        for (int c = wave; c < whole; c += waves) chunk(c, Int<4>{});
         // the last chunk may have 256 columns only
-        if ((g.P & 511) && whole % waves == wave) chunks(whole, Int<1>{}, Int<2>{});
+        if ((g.P & 511) && whole % waves == wave) chunk(whole, Int<2>{});
     }
     // lane holds columns 16 n + 4 q + v of row 16 m + i
 #pragma unroll
@@ -584,29 +573,34 @@ int64_t most_tiles(const c3::Mx4Gemm& g, int bm) {
     return g.M / bm + std::min<int64_t>(g.E + 1, g.M);
 }
 
-// Rows of the tile to use: 16, 32, 64 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile).
+// Rows of the tile to use: 16, 32 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile). Up to 32 rows the
+// weights' bytes decide and a larger tile would only idle. Past that, in us: a chunk (32 x 32
+// x 512) of mx4_gemm_rows takes a CU 0.6, whoever shares the CU; a round of tiles takes 6 + 0.3 per
+// 128 columns (256 rows) or 3.5 + 0.24 (128 rows, two to a CU). 64 rows: 2048x8192 13 us in tiles
+// of 32 against 19 of 128, 16384x16384 82 against 57, 28672x8192 70 against 37.
 int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
     const double rows = g.order ? (double)g.M / std::min(g.E, g.M) : g.M;  // of an expert, on average
     if (rows <= 16) return 16;
-    if (rows <= 32) return 32;
-    if (rows <= 64 || P < 512) return 64;
+    if (rows <= 32 || P < 512) return 32;
     auto tiles = [&](int bm) {
         const double m = g.order ? (double)g.M / bm + 0.5 * std::min(g.E, g.M) : (g.M + bm - 1) / bm;
         return m * ((g.N + bm - 1) / bm);
     };
     const double nk = P / 128;
-    const double t256 = std::ceil(tiles(256) / n_cu) * (18.0 + 0.9 * nk);
-    const double t128 = std::ceil(tiles(128) / (2 * n_cu)) * (10.0 + 0.7 * nk);
-    return t256 < t128 ? 256 : 128;
+    const double t256 = std::ceil(tiles(256) / n_cu) * (6.0 + 0.3 * nk);
+    const double t128 = std::ceil(tiles(128) / (2 * n_cu)) * (3.5 + 0.24 * nk);
+    const double t32 = std::ceil(tiles(32) * nk / 4 / n_cu) * 0.6;
+    return t32 < std::min(t128, t256) ? 32 : t256 < t128 ? 256 : 128;
 }
 
 template <int MT, int NT>
 c3_status launch_rows(const c3::Mx4Gemm& g, const Args& a, int n_cu, hipStream_t stream) {
     const int64_t groups = most_tiles(g, 16 * MT) * ((g.N + 16 * NT - 1) / (16 * NT));
     if (groups >= (1 << 22)) return c3::fail(C3_E_INVALID, "MX FP4 product: too many tiles");
-    // as many waves as there are chunks of K, up to what fills the device
-    int waves = 4;
-    while (waves < (MT * NT == 4 ? 16 : 8) && waves * groups < 16 * (int64_t)n_cu && waves * 512 < a.P)
+    // As many waves as fit the device at one time (24 a CU) with two chunks of K each at least, so
+    // that no second round of workgroups has part of the device to itself.
+    int waves = 1;
+    while (waves < (MT * NT == 4 ? 16 : 8) && 2 * waves * groups <= 24 * (int64_t)n_cu && waves * 1024 < a.P)
         waves *= 2;
     hipLaunchKernelGGL((mx4_gemm_rows<MT, NT>), dim3((unsigned)groups), dim3(64 * waves),
                        waves * 256 * MT * NT * sizeof(float), stream, a);
@@ -622,9 +616,7 @@ c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream) {
                     g.M, g.N, (int)mx4_padded(g.K), g.T, g.top_k, g.order ? g.E : 1,
                     (int)g.a_rows, (int)(g.dtype == C3_F32)};
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
-    int tile = choose_tile(g, a.P, n_cu);
-    const char* force = std::getenv("C3_MX4_TILE");  // tests: every kernel on every shape it can take
-    if (force && *force && (std::atoi(force) <= 64 || a.P >= 512)) tile = std::atoi(force);
+    const int tile = choose_tile(g, a.P, n_cu);
     if (tile >= 128) {
         const int64_t groups = most_tiles(g, tile) * ((g.N + tile - 1) / tile);
         if (groups >= (1 << 24)) return fail(C3_E_INVALID, "MX FP4 product: too many tiles");
@@ -632,12 +624,10 @@ c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream) {
             hipLaunchKernelGGL((mx4_gemm_tile<4, 4>), dim3((unsigned)groups), dim3(256), 0, stream, a);
         else
             hipLaunchKernelGGL((mx4_gemm_tile<2, 2>), dim3((unsigned)groups), dim3(256), 0, stream, a);
-    } else if (tile == 16) {
-        C3_TRY((launch_rows<1, 1>(g, a, n_cu, stream)));
     } else if (tile == 32) {
         C3_TRY((launch_rows<2, 2>(g, a, n_cu, stream)));
     } else {
-        C3_TRY((launch_rows<4, 4>(g, a, n_cu, stream)));
+        C3_TRY((launch_rows<1, 2>(g, a, n_cu, stream)));
     }
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;
