@@ -120,14 +120,12 @@ __device__ __forceinline__ float weight_of(const Args& g, int slot) {
 // a workgroup without a workspace. Operands go straight to registers: load j of a chunk takes
 // block 4 * j + l / 16 of row l % 16 (64 contiguous bytes of each row), which is the lane's operand
 // of matrix instruction j; the row's 16 scale bytes come as one load, of which the lane shifts out
-// byte 4 * j + l / 16. B is read once (non-temporal).
+// byte 4 * j + l / 16.
 template <int I>
 using Int = std::integral_constant<int, I>;
 
-template <bool STREAM>
 __device__ __forceinline__ i32x4_t load_piece(const uint8_t* p) {
-    const i32x4_t* q = reinterpret_cast<const i32x4_t*>(p);
-    return STREAM ? __builtin_nontemporal_load(q) : *q;
+    return *reinterpret_cast<const i32x4_t*>(p);
 }
 
 __device__ __forceinline__ f32x4_t mfma16(i32x4_t a, i32x4_t b, f32x4_t c, int sa, int sb) {
@@ -194,13 +192,13 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int j = 0; j < J; ++j) b[n][j] = load_piece<MT == 1>(pb[n] + (size_t)c * 256 + j * 64);
+                for (int j = 0; j < J; ++j) b[n][j] = load_piece(pb[n] + (size_t)c * 256 + j * 64);
                 sb[n].load(qb[n] + c * 16);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                for (int j = 0; j < J; ++j) a[m][j] = load_piece<false>(pa[m] + (size_t)c * 256 + j * 64);
+                for (int j = 0; j < J; ++j) a[m][j] = load_piece(pa[m] + (size_t)c * 256 + j * 64);
                 sa[m].load(qa[m] + c * 16);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -573,23 +571,29 @@ int64_t most_tiles(const c3::Mx4Gemm& g, int bm) {
     return g.M / bm + std::min<int64_t>(g.E + 1, g.M);
 }
 
-// Rows of the tile to use: 16, 32 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile). Up to 32 rows the
-// weights' bytes decide and a larger tile would only idle. Past that, in us: a chunk (32 x 32
-// x 512) of mx4_gemm_rows takes a CU 0.6, whoever shares the CU; a round of tiles takes 6 + 0.3 per
-// 128 columns (256 rows) or 3.5 + 0.24 (128 rows, two to a CU). 64 rows: 2048x8192 13 us in tiles
-// of 32 against 19 of 128, 16384x16384 82 against 57, 28672x8192 70 against 37.
+// Rows of the tile to use: 16, 32 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile). Up to 16 rows (8 of
+// an expert on average, since loads are uneven) the weights' bytes decide, and the smallest tile
+// keeps the most of them in flight. Past that, the least time in us of a model fitted to measured
+// times: a chunk (32 x 32 x 512) of mx4_gemm_rows takes a CU 0.55; a round of tiles takes a fixed
+// part and, per 128 columns, between `low` and `high` with the share of the device that it fills.
+// Measured: 64 rows x 2048x8192 13 us in tiles of 32 against 19 of 128, x 28672x8192 70 against 37;
+// 1024x4096x4096 17 us in tiles of 128 against 34 of 256, 2048x8192x8192 117 against 85.
 int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
-    const double rows = g.order ? (double)g.M / std::min(g.E, g.M) : g.M;  // of an expert, on average
-    if (rows <= 16) return 16;
-    if (rows <= 32 || P < 512) return 32;
+    const int used = std::min(g.E, g.M);  // experts with rows, at most
+    if (g.order ? g.M <= 8 * (int64_t)used : g.M <= 16) return 16;
+    if (P < 512) return 32;
     auto tiles = [&](int bm) {
-        const double m = g.order ? (double)g.M / bm + 0.5 * std::min(g.E, g.M) : (g.M + bm - 1) / bm;
+        const double m = g.order ? (double)g.M / bm + 0.6 * used : (g.M + bm - 1) / bm;
         return m * ((g.N + bm - 1) / bm);
     };
     const double nk = P / 128;
-    const double t256 = std::ceil(tiles(256) / n_cu) * (6.0 + 0.3 * nk);
-    const double t128 = std::ceil(tiles(128) / (2 * n_cu)) * (3.5 + 0.24 * nk);
-    const double t32 = std::ceil(tiles(32) * nk / 4 / n_cu) * 0.6;
+    auto rounds = [&](double n, double slots, double fixed, double low, double high) {
+        const double whole = std::floor(n / slots), rest = n - whole * slots;
+        return whole * (fixed + high * nk) + (rest > 0 ? fixed + (low + (high - low) * rest / slots) * nk : 0.0);
+    };
+    const double t256 = rounds(tiles(256), n_cu, 14.0, 0.5, 0.96);
+    const double t128 = rounds(tiles(128), 2 * n_cu, 5.0, 0.18, 0.8);
+    const double t32 = 4.0 + std::ceil(tiles(32) * nk / 4 / n_cu) * 0.55;
     return t32 < std::min(t128, t256) ? 32 : t256 < t128 ? 256 : 128;
 }
 
