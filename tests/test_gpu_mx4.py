@@ -73,6 +73,21 @@ def test_quantise(c3gpu, rows, cols, dtype, up, transpose):
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("rows,cols,ld", [(4097, 8190, 8192), (4100, 8193, 8196), (4096, 8192, 8193)])
+def test_quantise_large_transposed(c3gpu, rows, cols, ld, dtype):
+    """Sizes that take eight bytes of columns a lane, with ragged ends, and a stride that does not."""
+    import torch
+
+    rng = np.random.default_rng(rows + ld)
+    x = ref.bf16_round(rng.normal(0, 1, (rows, cols)).astype(np.float32))
+    codes, scales = quantise(c3gpu, x, dtype, False, True, ld)
+    some = np.concatenate([np.arange(300), np.arange(cols - 300, cols), rng.integers(0, cols, 200)])
+    want = ref.quantize(np.ascontiguousarray(x.T[some]))
+    np.testing.assert_array_equal(scales[some], want[1])
+    np.testing.assert_array_equal(codes[some], want[0])
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
 @pytest.mark.parametrize("transpose", [False, True])
 def test_quantise_every_rounding_border(c3gpu, dtype, transpose):
     """Every bf16 mantissa at each distance below the block's largest, for exponents over the
