@@ -238,25 +238,31 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 // Tile kernel
 // ------------------------------------------------------------------------------------------------
 // 4 waves (2 x 2), each 32*TM x 32*TN of C from v_mfma_scale_f32_32x32x64_f8f6f4 (lane l: row
-// l % 32, the block l / 32 of a 64-column slice, one scale byte). K goes in stages of 128 columns
-// (64 bytes of a row), four of them in LDS, filled by LDS-direct loads three stages ahead; scales
-// go in slabs of 1024 columns (32 bytes of a row: 64-byte requests would be wasted on less), two
-// of them in LDS. Half h of a wave takes the blocks 2h and 2h + 1 of a stage, so that slice j of
-// the stage is chunk 2h + j of its row.
+// l % 32, the block l / 32 of a 64-column slice, one scale byte). K goes in stages of 256 columns,
+// 128 bytes of a row: a whole line, since what bounds the kernel at full load is how many requests
+// a CU's vector cache keeps in flight, whatever their size (with 64-byte stages 2.1 us and 640
+// requests for 256 columns, 1.05 us of them matrix instructions; 8192x53248x16384 3.46 ms against
+// 3.07). Scales go in slabs of 1024 columns (32 bytes of a row, by two lanes), two of them in LDS.
+// Half h of a wave takes the blocks 2h and 2h + 1 of 128 columns, so that slice j is chunk 2h + j
+// of their half row.
 //
-// A stage is two slices of TM*TN matrix instructions. While those of one slice run, the wave reads
-// the next slice's fragments, and in the first of the two issues the loads of the stage three
-// ahead (its buffer's last reader finished before the previous stage's barrier). Everything is
-// slotted between matrix instructions by hand, since at TM = TN = 4 one wave per SIMD has nobody
-// to cover for it.
+// Two stages are in LDS, four where a CU has one workgroup of 128x128 to itself (`BUFS`). A stage
+// is four slices of TM*TN matrix instructions, one barrier before the last. While those of one
+// slice run, the wave reads the next slice's fragments; in the last and the next stage's first it
+// issues the loads that refill the buffer, one each `GAP` instructions (bunched, 2% slower).
+// Everything is slotted between matrix instructions by hand, since at TM = TN = 4 one wave per SIMD
+// has nobody to cover for it.
 //
-// The scales of two stages (8 bytes of a row) are read at once and permuted so that the byte of
-// slice j of stage s % 2 is byte 2 * (s % 2) + j of the lane's register, which the instruction
-// selects at no cost.
+// The scales of a stage (8 bytes of a row) are read at once and permuted so that the byte of slice
+// j of its half h is byte 2 * h + j of the lane's register, which the instruction selects at no
+// cost.
+//
+// Matrix instructions alone, operands in registers and random, run at 6.4 PFLOP/s here (power
+// holds the clock near 1.57 GHz; 9.7 on zeros).
 //
 // No load leaves its array: rows past M or N are clamped to a valid row, stages past the last one
 // load the last one again into a buffer nobody reads, and a scale unit (16 bytes) that would pass
-// the row's end starts 8 bytes earlier instead (its one pair of stages is then read 8 bytes later).
+// the row's end starts 8 bytes earlier instead (its one stage is then read 8 bytes later).
 #define C3_LDS __attribute__((address_space(3)))
 #define C3_WAIT_VMCNT(n) \
     __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
@@ -284,12 +290,9 @@ __device__ __forceinline__ void lds_load(i32x4_t r, uint32_t lds, uint32_t voff,
         : "memory", "m0");
 }
 
-// 16-byte chunk swizzle of 64-byte rows: chunk ^= 2*(r2^r3) + (r1^r2) (r_i = bit i of the row),
-// so that 8 or 16 lanes reading 16 bytes from consecutive rows hit distinct banks.
-__device__ __forceinline__ int swizzle(int row) {
-    const int b1 = (row >> 1) & 1, b2 = (row >> 2) & 1, b3 = (row >> 3) & 1;
-    return ((b2 ^ b3) << 1) | (b1 ^ b2);
-}
+// 16-byte chunk swizzle of 128-byte rows: chunk ^= swizzle(row), so that 8 or 16 lanes reading 16
+// bytes of the same chunk from consecutive rows hit distinct banks.
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 template <int BYTE>
 __device__ __forceinline__ f32x16_t mfma32(i32x4_t a, i32x4_t b, f32x16_t c, int sa, int sb) {
@@ -322,13 +325,14 @@ __device__ __forceinline__ void map_tile(int bid, int n, int tiles_m, int tiles_
     tn = in_group / rows;
 }
 
-template <int TM, int TN>
-__global__ __launch_bounds__(256, TM * TN == 16 ? 1 : 2) void mx4_gemm_tile(const Args g) {
+template <int TM, int TN, int BUFS>
+__global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_gemm_tile(const Args g) {
     constexpr int BM = 64 * TM, BN = 64 * TN, ROWS = BM + BN;
-    constexpr int STAGE = ROWS * 64, SCALES = 4 * STAGE, SLAB = ROWS * 32, UNIT = ROWS * 16;
+    constexpr int STAGE = ROWS * 128, SCALES = BUFS * STAGE, SLAB = ROWS * 32;
     constexpr int NM = TM * TN, NF = TM + TN;  // matrix instructions of a slice, fragments
-    constexpr int NS = (TM + TN) / 4;          // 64-row groups of scales a wave loads
-    constexpr int LOADS = TM + TN;             // code loads of a wave and stage
+    constexpr int NS = (TM + TN) / 2;          // 32-row groups of scales a wave loads
+    constexpr int LOADS = 2 * (TM + TN);       // code loads of a wave and stage
+    constexpr int GAP = 2 * NM / LOADS;        // matrix instructions between two of them
     __shared__ __attribute__((aligned(1024))) char smem[SCALES + 2 * SLAB];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -366,140 +370,156 @@ __global__ __launch_bounds__(256, TM * TN == 16 ? 1 : 2) void mx4_gemm_tile(cons
         };
         auto b_row = [&](int i) -> uint32_t { return (uint32_t)min(i, g.N - 1 - n0); };
 
-        // block i of wave w: rows 16 * (T * w + i) + lane / 4, chunk lane % 4
-        uint32_t va[TM], vb[TN], vs[NS];
-        const int q = lane >> 2;
-        const uint32_t chunk = (uint32_t)((lane & 3) ^ swizzle(q)) * 16u;
+        // load i of wave w: rows 8 * (2 * T * w + i) + lane / 8, chunk lane % 8
+        uint32_t va[2 * TM], vb[2 * TN], vs[NS];
+        const int q = lane >> 3;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) va[i] = a_row(16 * (TM * wave + i) + q) * code_row + chunk;
+        for (int i = 0; i < 2 * TM; ++i)
+            va[i] = a_row(8 * (2 * TM * wave + i) + q) * code_row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) vb[i] = b_row(16 * (TN * wave + i) + q) * code_row + chunk;
+        for (int i = 0; i < 2 * TN; ++i)
+            vb[i] = b_row(8 * (2 * TN * wave + i) + q) * code_row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
+        // scales: load i of wave w: rows 32 * (w + 4 * i) + lane / 2, unit (lane % 2) ^ (bit 2 of the row)
         bool s_is_a[NS];
+        const uint32_t unit = (uint32_t)((lane & 1) ^ ((lane >> 3) & 1)) * 16u;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-            const int first = 64 * (wave + 4 * i);
+            const int first = 32 * (wave + 4 * i);
             s_is_a[i] = first < BM;
-            vs[i] = (s_is_a[i] ? a_row(first + lane) : b_row(first - BM + lane)) * scale_row;
+            vs[i] = (s_is_a[i] ? a_row(first + (lane >> 1)) : b_row(first - BM + (lane >> 1))) * scale_row;
         }
         const uint32_t lds0 = (uint32_t)(uintptr_t)(C3_LDS char*)smem;
-        auto load_codes = [&](uint32_t k, int st, int i) {  // load i of stage k into buffer st
-            const uint32_t soff = min(k, nk - 1) * 64u;
-            const uint32_t at = lds0 + (uint32_t)(st * STAGE);
-            if (i < TM) lds_load(rA, at + (uint32_t)((TM * wave + i) * 1024), va[i < TM ? i : 0], soff);
-            else lds_load(rB, at + (uint32_t)(BM * 64 + (TN * wave + i - TM) * 1024), vb[i < TM ? 0 : i - TM], soff);
+        auto load_codes = [&](uint32_t stage, int buf, int i) {  // load i of a stage into a buffer
+            const uint32_t soff = min(stage, pairs - 1) * 128u;
+            const uint32_t at = lds0 + (uint32_t)(buf * STAGE);
+            if (i < 2 * TM) lds_load(rA, at + (uint32_t)((2 * TM * wave + i) * 1024), va[i < 2 * TM ? i : 0], soff);
+            else lds_load(rB, at + (uint32_t)(BM * 128 + (2 * TN * wave + i - 2 * TM) * 1024), vb[i < 2 * TM ? 0 : i - 2 * TM], soff);
         };
         auto load_scales = [&](uint32_t slab, int buf) {
+            const uint32_t in_row = min(slab * 32u + unit, scale_row - 16u);
 #pragma unroll
-            for (int i = 0; i < NS; ++i)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t soff = min(slab * 32u + 16u * u, scale_row - 16u);
-                    const uint32_t at = lds0 + (uint32_t)(SCALES + u * UNIT + (wave + 4 * i) * 1024) +
-                                        (uint32_t)buf * SLAB;
-                    lds_load(s_is_a[i] ? rsA : rsB, at, vs[i], soff);
-                }
+            for (int i = 0; i < NS; ++i) {
+                const uint32_t at = lds0 + (uint32_t)(SCALES + (wave + 4 * i) * 1024) + (uint32_t)buf * SLAB;
+                lds_load(s_is_a[i] ? rsA : rsB, at, vs[i] + in_row, 0);
+            }
         };
 
-        // fragment reads: f < TM of A, then of B
+        // fragment reads: f < TM of A, then of B; half HALF of a stage, slice j of it
         const char* lds = smem;
-        uint32_t f_at[2];
+        uint32_t f_at[2][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            f_at[j] = (uint32_t)row32 * 64u + (uint32_t)(((2 * half + j) ^ swizzle(row32)) << 4);
-        const uint32_t fa = (uint32_t)(wm * 32 * TM) * 64u, fb = (uint32_t)(BM + wn * 32 * TN) * 64u;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                f_at[h][j] = (uint32_t)row32 * 128u + (uint32_t)(((4 * h + 2 * half + j) ^ swizzle(row32)) << 4);
+        const uint32_t fa = (uint32_t)(wm * 32 * TM) * 128u, fb = (uint32_t)(BM + wn * 32 * TN) * 128u;
         i32x4_t frag[2][NF];
-        auto read_frag = [&](int st, int j, int f) {
-            const uint32_t at = (uint32_t)(st * STAGE) + (f < TM ? fa + f * 2048u : fb + (f - TM) * 2048u) + f_at[j];
+        auto read_frag = [&](int buf, int h, int j, int f) {
+            const uint32_t at = (uint32_t)(buf * STAGE) + (f < TM ? fa + f * 4096u : fb + (f - TM) * 4096u) + f_at[h][j];
             frag[j][f] = *reinterpret_cast<const C3_LDS i32x4_t*>((const C3_LDS char*)lds + at);
         };
         const uint32_t sel = half ? 0x07060302u : 0x05040100u;
-        const uint32_t sfa = (uint32_t)(SCALES + (wm * 32 * TM + row32) * 16);
-        const uint32_t sfb = (uint32_t)(SCALES + (BM + wn * 32 * TN + row32) * 16);
+        const uint32_t sfa = (uint32_t)(SCALES + (wm * 32 * TM + row32) * 32);
+        const uint32_t sfb = (uint32_t)(SCALES + (BM + wn * 32 * TN + row32) * 32);
+        const uint32_t flip = (uint32_t)((row32 >> 2) & 1) * 16u;
         i32x2_t raw[NF];
         int sc[2][NF];
         auto read_scale = [&](uint32_t at, int f) {
-            const uint32_t o = at + (f < TM ? sfa + f * 512u : sfb + (f - TM) * 512u);
+            const uint32_t o = (at ^ flip) + (f < TM ? sfa + f * 1024u : sfb + (f - TM) * 1024u);
             raw[f] = *reinterpret_cast<const C3_LDS i32x2_t*>((const C3_LDS char*)lds + o);
         };
         auto permute = [&](int set, int f) {
             sc[set][f] = (int)__builtin_amdgcn_perm((uint32_t)raw[f].y, (uint32_t)raw[f].x, sel);
         };
-        // where the scales of pair p are, in the slab buffers
+        // where the scales of stage p are, in the slab buffers
         auto pair_at = [&](uint32_t p) -> uint32_t {
-            return ((p >> 2) & 1) * SLAB + ((p >> 1) & 1) * UNIT + ((p & 1) | (p == pairs - 1)) * 8u;
+            return ((p >> 2) & 1) * SLAB + ((p >> 1) & 1) * 16u + ((p & 1) | (p == pairs - 1)) * 8u;
         };
 
-        // One stage. st: its buffer; PAR: kt % 2; SET: the scales' register set; AHEAD: loads that
-        // may still be in flight when stage kt + 1 has to have landed; SLABS: issue the next slab.
-        auto step = [&](uint32_t kt, int st, auto par_c, auto set_c, auto ahead_c, auto slabs_c) {
-            constexpr int PAR = decltype(par_c)::value, SET = decltype(set_c)::value;
-            constexpr int AHEAD = decltype(ahead_c)::value;
+        // One stage p in buffer `buf`, its scales in register set SET: four slices of NM matrix
+        // instructions. The last one and the next stage's first issue the loads of stage p + BUFS
+        // into `buf`, whose last reader finished before the barrier. AHEAD: loads that may still be
+        // in flight there; SLABS: issue the next slab of scales.
+        auto mma = [&](int i, auto h_c, auto j_c, auto set_c) {
+            constexpr int H = decltype(h_c)::value, J = decltype(j_c)::value, SET = decltype(set_c)::value;
+            const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
+            acc[mi][ni] = mfma32<2 * H + J>(frag[J][TM + ni], frag[J][mi], acc[mi][ni], sc[SET][TM + ni], sc[SET][mi]);
+        };
+        auto stage = [&](uint32_t p, int buf, auto set_c, auto slabs_c, auto ahead_c) {
+            constexpr int SET = decltype(set_c)::value;
             constexpr bool SLABS = decltype(slabs_c)::value != 0;
-            const uint32_t next_pair = pair_at((kt + 1) >> 1);
+            const uint32_t next_pair = pair_at(p + 1);
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
-                const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
-                acc[mi][ni] = mfma32<2 * PAR>(frag[0][TM + ni], frag[0][mi], acc[mi][ni], sc[SET][TM + ni], sc[SET][mi]);
-                if (i < NF) read_frag(st, 1, i);
-                if (NM == 4) load_codes(kt + 3, (st + 3) & 3, i);
-                else if (i >= NM - LOADS) load_codes(kt + 3, (st + 3) & 3, i - (NM - LOADS));
+                mma(i, Int<0>{}, Int<0>{}, set_c);
+                if (i < NF) read_frag(buf, 0, 1, i);
+                if (i % GAP == GAP - 1) load_codes(p + BUFS - 1, (buf + BUFS - 1) & (BUFS - 1), LOADS / 2 + i / GAP);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (SLABS) load_scales((kt >> 3) + 1, (int)(((kt >> 3) + 1) & 1));
-            C3_WAIT_VMCNT(AHEAD);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                mma(i, Int<0>{}, Int<1>{}, set_c);
+                if (i < NF) read_frag(buf, 1, 0, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                mma(i, Int<1>{}, Int<0>{}, set_c);
+                if (i < NF) read_frag(buf, 1, 1, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            C3_WAIT_VMCNT(decltype(ahead_c)::value);
             __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
+            if (SLABS) load_scales((p >> 2) + 1, (int)(((p >> 2) + 1) & 1));
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
-                const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
-                acc[mi][ni] = mfma32<2 * PAR + 1>(frag[1][TM + ni], frag[1][mi], acc[mi][ni], sc[SET][TM + ni],
-                                                  sc[SET][mi]);
+                mma(i, Int<1>{}, Int<1>{}, set_c);
                 if (i < NF) {
-                    if (PAR) read_scale(next_pair, i);
-                    read_frag((st + 1) & 3, 0, i);
+                    read_scale(next_pair, i);
+                    read_frag((buf + 1) & (BUFS - 1), 0, 0, i);
                 }
-                if (PAR && NM == 16 && i >= 8) permute(SET ^ 1, i - 8);
+                if (i % GAP == 0) load_codes(p + BUFS, buf, i / GAP);
+                if (NM == 16 && i >= 8) permute(SET ^ 1, i - 8);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (PAR && NM != 16)
+            if (NM != 16)
 #pragma unroll
                 for (int f = 0; f < NF; ++f) permute(SET ^ 1, f);
         };
 
         load_scales(0, 0);
 #pragma unroll
-        for (int s = 0; s < 3; ++s)
+        for (int st = 0; st < BUFS - 1; ++st)
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) load_codes(s, s, i);
-        C3_WAIT_VMCNT(2 * LOADS);
+            for (int i = 0; i < LOADS; ++i) load_codes(st, st, i);
+#pragma unroll
+        for (int i = 0; i < LOADS / 2; ++i) load_codes(BUFS - 1, BUFS - 1, i);
+        C3_WAIT_VMCNT((BUFS - 2) * LOADS + LOADS / 2);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
             read_scale(pair_at(0), f);
-            read_frag(0, 0, f);
+            read_frag(0, 0, 0, f);
         }
 #pragma unroll
         for (int f = 0; f < NF; ++f) permute(0, f);
 
-        // The next slab's loads go out in step 1 of eight, after those of stage 4: they are among
-        // the loads in flight at steps 1 (just issued) and 2.
-        constexpr int L2 = 2 * LOADS, LS = 2 * LOADS + 2 * NS;
-        uint32_t kt = 0;
-        for (; kt + 8 <= nk; kt += 8) {
-            step(kt, 0, Int<0>{}, Int<0>{}, Int<L2>{}, Int<0>{});
-            step(kt + 1, 1, Int<1>{}, Int<0>{}, Int<LS>{}, Int<1>{});
-            step(kt + 2, 2, Int<0>{}, Int<1>{}, Int<LS>{}, Int<0>{});
-            step(kt + 3, 3, Int<1>{}, Int<1>{}, Int<L2>{}, Int<0>{});
-            step(kt + 4, 0, Int<0>{}, Int<0>{}, Int<L2>{}, Int<0>{});
-            step(kt + 5, 1, Int<1>{}, Int<0>{}, Int<L2>{}, Int<0>{});
-            step(kt + 6, 2, Int<0>{}, Int<1>{}, Int<L2>{}, Int<0>{});
-            step(kt + 7, 3, Int<1>{}, Int<1>{}, Int<L2>{}, Int<0>{});
+        // The next slab's loads go out in the first stage of four, after those of stage p + BUFS - 1;
+        // loads in flight when stage p + 1 has to have landed: those of p + 2 .. p + BUFS - 1, with
+        // two buffers none.
+        constexpr int L = (BUFS - 2) * LOADS, LS = BUFS > 2 ? L + NS : 0;
+        uint32_t p = 0;
+        for (; p + 4 <= pairs; p += 4) {
+            stage(p, 0, Int<0>{}, Int<1>{}, Int<L>{});
+            stage(p + 1, 1, Int<1>{}, Int<0>{}, Int<LS>{});
+            stage(p + 2, 2 & (BUFS - 1), Int<0>{}, Int<0>{}, Int<LS>{});
+            stage(p + 3, 3 & (BUFS - 1), Int<1>{}, Int<0>{}, Int<L>{});
         }
-        for (; kt < nk; kt += 2) {
-            step(kt, (int)(kt & 3), Int<0>{}, Int<0>{}, Int<L2>{}, Int<0>{});
-            step(kt + 1, (int)((kt + 1) & 3), Int<1>{}, Int<0>{}, Int<L2>{}, Int<0>{});
+        for (; p < pairs; ++p) {
+            stage(p, (int)(p & (BUFS - 1)), Int<0>{}, Int<0>{}, Int<L>{});
 #pragma unroll
             for (int f = 0; f < NF; ++f) sc[0][f] = sc[1][f];
         }
@@ -571,28 +591,33 @@ int64_t most_tiles(const c3::Mx4Gemm& g, int bm) {
     return g.M / bm + std::min<int64_t>(g.E + 1, g.M);
 }
 
+// Square tiles of `bm` that the product takes; with experts, whose loads the host does not know, an
+// estimate: each one that has rows leaves a tile partly filled.
+double tiles_of(const c3::Mx4Gemm& g, int bm) {
+    const int used = std::min(g.E, g.M);  // experts with rows, at most
+    const double m = g.order ? (double)g.M / bm + 0.6 * used : (g.M + bm - 1) / bm;
+    return m * ((g.N + bm - 1) / bm);
+}
+
 // Rows of the tile to use: 16, 32 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile). Up to 16 rows (8 of
 // an expert on average, since loads are uneven) the weights' bytes decide, and the smallest tile
 // keeps the most of them in flight. Past that, the least time in us of a model fitted to measured
 // times: a chunk (32 x 32 x 512) of mx4_gemm_rows takes a CU 0.55; a round of tiles takes a fixed
 // part and, per 128 columns, between `low` and `high` with the share of the device that it fills.
 // Measured: 64 rows x 2048x8192 13 us in tiles of 32 against 19 of 128, x 28672x8192 70 against 37;
-// 1024x4096x4096 17 us in tiles of 128 against 34 of 256, 2048x8192x8192 117 against 85.
+// 1024x4096x4096 15 us in tiles of 128 against 34 of 256.
 int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
-    const int used = std::min(g.E, g.M);  // experts with rows, at most
+    const int used = std::min(g.E, g.M);
     if (g.order ? g.M <= 8 * (int64_t)used : g.M <= 16) return 16;
     if (P < 512) return 32;
-    auto tiles = [&](int bm) {
-        const double m = g.order ? (double)g.M / bm + 0.6 * used : (g.M + bm - 1) / bm;
-        return m * ((g.N + bm - 1) / bm);
-    };
+    auto tiles = [&](int bm) { return tiles_of(g, bm); };
     const double nk = P / 128;
     auto rounds = [&](double n, double slots, double fixed, double low, double high) {
         const double whole = std::floor(n / slots), rest = n - whole * slots;
         return whole * (fixed + high * nk) + (rest > 0 ? fixed + (low + (high - low) * rest / slots) * nk : 0.0);
     };
-    const double t256 = rounds(tiles(256), n_cu, 14.0, 0.5, 0.96);
-    const double t128 = rounds(tiles(128), 2 * n_cu, 5.0, 0.18, 0.8);
+    const double t256 = rounds(tiles(256), n_cu, 16.0, 0.4, 0.77);
+    const double t128 = rounds(tiles(128), 2 * n_cu, g.order ? 8.0 : 5.0, 0.16, 0.7);
     const double t32 = 4.0 + std::ceil(tiles(32) * nk / 4 / n_cu) * 0.55;
     return t32 < std::min(t128, t256) ? 32 : t256 < t128 ? 256 : 128;
 }
@@ -624,10 +649,10 @@ c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream) {
     if (tile >= 128) {
         const int64_t groups = most_tiles(g, tile) * ((g.N + tile - 1) / tile);
         if (groups >= (1 << 24)) return fail(C3_E_INVALID, "MX FP4 product: too many tiles");
-        if (tile == 256)
-            hipLaunchKernelGGL((mx4_gemm_tile<4, 4>), dim3((unsigned)groups), dim3(256), 0, stream, a);
-        else
-            hipLaunchKernelGGL((mx4_gemm_tile<2, 2>), dim3((unsigned)groups), dim3(256), 0, stream, a);
+        // 128 rows: four stages in LDS where that costs no CU its second workgroup
+        auto kernel = tile == 256 ? mx4_gemm_tile<4, 4, 2>
+                      : tiles_of(g, 128) <= n_cu ? mx4_gemm_tile<2, 2, 4> : mx4_gemm_tile<2, 2, 2>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(256), 0, stream, a);
     } else if (tile == 32) {
         C3_TRY((launch_rows<2, 2>(g, a, n_cu, stream)));
     } else {

@@ -201,6 +201,19 @@ def test_product(c3gpu, M, N, K, dtype):
     assert (got[M:] == -7.0).all() and (got[:, N:] == -7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(2049, 4100, 8200), (2300, 4097, 7700), (1500, 4200, 600), (40, 33000, 900)])
+def test_product_large(c3gpu, M, N, K, dtype):
+    """Sizes past one round of tiles of 256 and of 128, and rows that share a tile with none."""
+    test_product(c3gpu, M, N, K, dtype)
+
+
+@pytest.mark.parametrize("K", [512, 700, 1000, 1025, 1300, 2000, 2300])
+def test_product_lengths_of_k(c3gpu, K):
+    """Every remainder of the stages of 256 columns, at a size with a tile for about half the CUs."""
+    test_product(c3gpu, 400, 4200, K, 0)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 70, 600), (100, 300, 1500), (520, 700, 700), (2050, 2300, 520)])
 def test_product_integers_exact_and_repeatable(c3gpu, M, N, K):
     """Small integer values: every partial sum is exact in fp32, so the product is too; and the
@@ -317,6 +330,11 @@ def test_experts(c3gpu, T, E, k, N, K, skew, absent, per_slot, weighted, dtype):
     assert (got[-1] == -7.0).all() and (got[:, N:] == -7.0).all()
     absent_slots = order[offsets[E]:]
     assert (got[absent_slots, :N] == 0).all()
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+def test_experts_large(c3gpu, per_slot):
+    test_experts(c3gpu, 4100, 3, 1, 2100, 6000, 0.3, 0.02, per_slot, True, 0)
 
 
 def test_experts_never_follow_bad_plans(c3gpu):
