@@ -530,59 +530,71 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
     // ---- C: 32 rows at a time through LDS (this wave's own 17 KiB), so that it leaves in whole
     // 128-byte lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each
     // 32 x 32 block; a row's 16-byte chunks are permuted by its number against bank conflicts.
-    const int size = g.f32 ? 4 : 2;
-    const int row_bytes = 32 * TN * size, chunks = row_bytes / 16;
-    char* out = smem + wave * (32 * 32 * TN * 4 + 32 * 4);
+    int slot[TM];
+    float weight[TM];
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi) slot[mi] = slot_at(g, r.begin + wm * 32 * TM + mi * 32 + row32, r.end);
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi) weight[mi] = weight_of(g, slot[mi]);
+    char* out = smem + wave * (32 * 32 * TN * 4 + 32 * 4 * TM);
     int* slots = reinterpret_cast<int*>(out + 32 * 32 * TN * 4);
-    const bool aligned = (((uintptr_t)g.C | (uint64_t)g.ldc * size) & 15) == 0;
+    if (half == 0)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) slots[mi * 32 + row32] = slot[mi];
     const int nw = n0 + wn * 32 * TN;
+    auto store = [&](auto f32_c) {
+        constexpr bool F32 = decltype(f32_c)::value != 0;
+        constexpr int size = F32 ? 4 : 2, row_bytes = 32 * TN * size, chunks = row_bytes / 16;
+        const bool aligned = (((uintptr_t)g.C | (uint64_t)g.ldc * size) & 15) == 0;
 #pragma unroll
-    for (int mi = 0; mi < TM; ++mi) {
-        const int slot = slot_at(g, r.begin + wm * 32 * TM + mi * 32 + row32, r.end);
-        const float w = weight_of(g, slot);
-        if (half == 0) slots[row32] = slot;
+        for (int mi = 0; mi < TM; ++mi) {
 #pragma unroll
-        for (int ni = 0; ni < TN; ++ni)
+            for (int ni = 0; ni < TN; ++ni)
 #pragma unroll
-            for (int v = 0; v < 16; v += 4) {
-                const int n = 32 * ni + 2 * v + 4 * half;
-                f32x4_t y;
+                for (int v = 0; v < 16; v += 4) {
+                    const int n = 32 * ni + 2 * v + 4 * half;
+                    f32x4_t y;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = r.expert < g.E ? w * acc[mi][ni][v + i] : 0.f;
-                if (g.f32) {
-                    const int c = (n / 4) ^ (row32 & (chunks - 1));
-                    *reinterpret_cast<f32x4_t*>(out + row32 * row_bytes + c * 16) = y;
+                    for (int i = 0; i < 4; ++i) y[i] = r.expert < g.E ? weight[mi] * acc[mi][ni][v + i] : 0.f;
+                    if constexpr (F32) {
+                        const int c = (n / 4) ^ (row32 & (chunks - 1));
+                        *reinterpret_cast<f32x4_t*>(out + row32 * row_bytes + c * 16) = y;
+                    } else {
+                        const int c = (n / 8) ^ (row32 & (chunks - 1));
+                        bf16x4_t b = {static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
+                                      static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
+                        *reinterpret_cast<bf16x4_t*>(out + row32 * row_bytes + c * 16 + (n & 4) * 2) = b;
+                    }
+                }
+            own_lds_fence();
+            constexpr int EACH = chunks / 2;  // of a lane
+#pragma unroll
+            for (int u = 0; u < EACH; ++u) {
+                const int i = u * 64 + lane, m = i / chunks, c = i % chunks, s = slots[mi * 32 + m];
+                const int n = nw + c * (16 / size);
+                if (s < 0 || n >= g.N) continue;
+                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(out + m * row_bytes + (c ^ (m & (chunks - 1))) * 16);
+                char* p = static_cast<char*>(g.C) + ((size_t)s * g.ldc + n) * size;
+                const int fit = (g.N - n) * size;
+                if (fit >= 16 && aligned) {
+                    *reinterpret_cast<i32x4_t*>(p) = v;
+                } else if (fit >= 16) {
+                    __builtin_memcpy(__builtin_assume_aligned(p, 2), &v, 16);
+                } else if constexpr (F32) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e * 4 < fit) reinterpret_cast<int*>(p)[e] = v[e];
                 } else {
-                    const int c = (n / 8) ^ (row32 & (chunks - 1));
-                    bf16x4_t b = {static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
-                                  static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
-                    *reinterpret_cast<bf16x4_t*>(out + row32 * row_bytes + c * 16 + (n & 4) * 2) = b;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e * 2 < fit) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
                 }
             }
-        own_lds_fence();
-        for (int i = lane; i < 32 * chunks; i += 64) {
-            const int m = i / chunks, c = i % chunks, s = slots[m];
-            const int n = nw + c * (16 / size);
-            if (s < 0 || n >= g.N) continue;
-            const i32x4_t v = *reinterpret_cast<const i32x4_t*>(out + m * row_bytes + (c ^ (m & (chunks - 1))) * 16);
-            char* p = static_cast<char*>(g.C) + ((size_t)s * g.ldc + n) * size;
-            const int fit = (g.N - n) * size;
-            if (fit >= 16 && aligned) {
-                *reinterpret_cast<i32x4_t*>(p) = v;
-            } else if (fit >= 16) {
-                __builtin_memcpy(__builtin_assume_aligned(p, 2), &v, 16);
-            } else if (g.f32) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e * 4 < fit) reinterpret_cast<int*>(p)[e] = v[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e * 2 < fit) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
-            }
+            own_lds_fence();
         }
-        own_lds_fence();
-    }
+    };
+    if (g.f32) store(Int<1>{});
+    else store(Int<0>{});
 }
 
 // Most tiles of `bm` rows that the order can need.
