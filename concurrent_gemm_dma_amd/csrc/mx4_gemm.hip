@@ -262,7 +262,8 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 //
 // No load leaves its array: rows past M or N are clamped to a valid row, stages past the last one
 // load the last one again into a buffer nobody reads, and a scale unit (16 bytes) that would pass
-// the row's end starts 8 bytes earlier instead (its one stage is then read 8 bytes later).
+// the row's end starts 8 bytes earlier instead (its one stage is then read 8 bytes later; rows of
+// 256 columns have no second unit, and their scales skip LDS).
 #define C3_LDS __attribute__((address_space(3)))
 #define C3_WAIT_VMCNT(n) \
     __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
@@ -489,7 +490,7 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
                 for (int f = 0; f < NF; ++f) permute(SET ^ 1, f);
         };
 
-        load_scales(0, 0);
+        if (pairs > 1) load_scales(0, 0);
 #pragma unroll
         for (int st = 0; st < BUFS - 1; ++st)
 #pragma unroll
@@ -501,8 +502,16 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            read_scale(pair_at(0), f);
+            if (pairs > 1) read_scale(pair_at(0), f);
             read_frag(0, 0, 0, f);
+        }
+        if (pairs == 1) {  // rows of one unit's half: straight from memory
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const uint8_t* p = f < TM ? g.sA + (a_base + a_row(wm * 32 * TM + f * 32 + row32)) * 8
+                                          : g.sB + (b_base + b_row(wn * 32 * TN + (f - TM) * 32 + row32)) * 8;
+                raw[f] = *reinterpret_cast<const i32x2_t*>(p);
+            }
         }
 #pragma unroll
         for (int f = 0; f < NF; ++f) permute(0, f);
@@ -621,7 +630,6 @@ double tiles_of(const c3::Mx4Gemm& g, int bm) {
 int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
     const int used = std::min(g.E, g.M);
     if (g.order ? g.M <= 8 * (int64_t)used : g.M <= 16) return 16;
-    if (P < 512) return 32;
     auto tiles = [&](int bm) { return tiles_of(g, bm); };
     const double nk = P / 128;
     auto rounds = [&](double n, double slots, double fixed, double low, double high) {

@@ -214,6 +214,12 @@ def test_product_lengths_of_k(c3gpu, K):
     test_product(c3gpu, 400, 4200, K, 0)
 
 
+@pytest.mark.parametrize("M,N,K", [(700, 2000, 128), (301, 4001, 256), (2500, 5003, 200), (129, 9000, 1)])
+def test_product_short_rows(c3gpu, M, N, K):
+    """K within one unit of 256 columns, in tiles of 128: one for half the CUs, and two to a CU."""
+    test_product(c3gpu, M, N, K, 0)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 70, 600), (100, 300, 1500), (520, 700, 700), (2050, 2300, 520)])
 def test_product_integers_exact_and_repeatable(c3gpu, M, N, K):
     """Small integer values: every partial sum is exact in fp32, so the product is too; and the
@@ -335,6 +341,10 @@ def test_experts(c3gpu, T, E, k, N, K, skew, absent, per_slot, weighted, dtype):
 @pytest.mark.parametrize("per_slot", [False, True])
 def test_experts_large(c3gpu, per_slot):
     test_experts(c3gpu, 4100, 3, 1, 2100, 6000, 0.3, 0.02, per_slot, True, 0)
+
+
+def test_experts_short_rows(c3gpu):
+    test_experts(c3gpu, 1000, 16, 2, 2001, 256, 0.5, 0.05, False, True, 1)
 
 
 def test_experts_never_follow_bad_plans(c3gpu):
