@@ -121,6 +121,10 @@ __device__ __forceinline__ float weight_of(const Args& g, int slot) {
 // block 4 * j + l / 16 of row l % 16 (64 contiguous bytes of each row), which is the lane's operand
 // of matrix instruction j; the row's 16 scale bytes come as one load, of which the lane shifts out
 // byte 4 * j + l / 16.
+//
+// Bound by B's bytes: 1x28672x8192 24 us alone (5.2 TB/s), 32 experts' 4096x4096 with eight tokens'
+// choices 24-33. Loads of 16 bytes a row at a stride of 64 took a third longer, two column blocks a
+// workgroup beat one and four, and more loads in flight a wave do not pay (they cost waves).
 template <int I>
 using Int = std::integral_constant<int, I>;
 
@@ -241,8 +245,8 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 // l % 32, the block l / 32 of a 64-column slice, one scale byte). K goes in stages of 256 columns,
 // 128 bytes of a row: a whole line, since what bounds the kernel at full load is how many requests
 // a CU's vector cache keeps in flight, whatever their size (with 64-byte stages 2.1 us and 640
-// requests for 256 columns, 1.05 us of them matrix instructions; 8192x53248x16384 3.46 ms against
-// 3.07). Scales go in slabs of 1024 columns (32 bytes of a row, by two lanes), two of them in LDS.
+// requests for 128 columns, of which half a microsecond matrix instructions; 8192x53248x16384 3.46
+// ms against 3.07). Scales go in slabs of 1024 columns (32 bytes of a row, by two lanes), two of them in LDS.
 // Half h of a wave takes the blocks 2h and 2h + 1 of 128 columns, so that slice j is chunk 2h + j
 // of their half row.
 //
@@ -257,8 +261,10 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 // j of its half h is byte 2 * h + j of the lane's register, which the instruction selects at no
 // cost.
 //
-// Matrix instructions alone, operands in registers and random, run at 6.4 PFLOP/s here (power
-// holds the clock near 1.57 GHz; 9.7 on zeros).
+// 8192x53248x16384 2.97 ms, 4.8 PFLOP/s; 8192x8192x8192 0.26 ms with the matrix pipe busy 60% of
+// the cycles at 1.72 GHz. Matrix instructions alone, operands in registers and random, run at 6.4
+// PFLOP/s here (power holds the clock near 1.57 GHz; 9.7 on zeros). A tile's start and end cost a
+// CU 12-16 us, which short K shows: 8192 slots of 8 experts x 14336x4096 0.62 ms, 3.1 PFLOP/s.
 //
 // No load leaves its array: rows past M or N are clamped to a valid row, stages past the last one
 // load the last one again into a buffer nobody reads, and a scale unit (16 bytes) that would pass

@@ -167,6 +167,10 @@ struct Choice {
 // round of the choice is one reduction over the lanes' largest keys; the lane that had it shifts
 // its list. Scores in 64 bits are computed only where the choice needs them (with a bias, or for
 // the two best of a group); weights in 32.
+//
+// Bound by instructions: 32768 tokens of 128 experts, bf16, 8 each 11-12 us, of 256 experts in 8
+// groups with a bias 47 us (a 64-bit exponential for every expert); one token of those 4.2 us,
+// memory latencies and the rounds in turn.
 template <typename T, int W, int NV, bool BIAS>
 __global__ __launch_bounds__(256) void route_tokens(const T* __restrict__ logits, const Choice c,
                                                     const float* __restrict__ bias,
@@ -321,7 +325,9 @@ __global__ __launch_bounds__(256) void route_tokens(const T* __restrict__ logits
 
 // One wave per token; lane j holds the j-th choice, value i of a lane is expert 64 * i + lane.
 // sigmoid: dl = g s (1 - s), renormalised (1 - s) w (g - sum g w); softmax: p (g - sum g p) over
-// all in reach, renormalised the same over the chosen alone.
+// all in reach, renormalised the same over the chosen alone. 8192 tokens of 256 experts, bf16, 6.7 us,
+// of which a launch is 2 and the bytes at a copy's rate 1.4: the rest is the chain of a wave's loads
+// (index, logit) and reductions.
 template <typename T, int NV>
 __global__ __launch_bounds__(256) void route_gradient(const T* __restrict__ logits,
                                                       int64_t n_tokens, int E, int64_t ld,
@@ -408,7 +414,8 @@ __global__ __launch_bounds__(256) void route_gradient(const T* __restrict__ logi
 // consecutive choices, each of its waves a run of them. Counts per expert of every workgroup
 // (plan_count), then every workgroup adds up what lies before its own choices and places them
 // (plan_place): rank = expert's first position + choices of earlier workgroups + of earlier waves +
-// of earlier lanes, so the order is that of f.
+// of earlier lanes, so the order is that of f. One token 2.0 us; 32768 tokens of 8 choices, 128
+// experts 3.5 + 10.4 us, the second bound by its chain of passes over LDS.
 constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves;
 constexpr int kMaxGroups = 128;
 constexpr int kMaxBins = C3_MAX_EXPERTS + 1;  // the last one in use: slots without an expert
