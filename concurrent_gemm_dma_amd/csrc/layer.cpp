@@ -218,11 +218,13 @@ c3_status c3_route_plan(const int32_t* idx, int64_t n_tokens, int top_k, int n_e
 }
 
 c3_status c3_mx4_bytes(int64_t rows, int64_t cols, size_t* codes, size_t* scales) {
-    C3_TRY(check_operand("c3_mx4_bytes", rows, cols));
-    if (cols < 1) return fail(C3_E_INVALID, "c3_mx4_bytes: cols must be at least 1");
-    if (codes) *codes = codes_bytes(rows, cols);
-    if (scales) *scales = scales_bytes(rows, cols);
-    return C3_OK;
+    C3_ENTRY({
+        C3_TRY(check_operand("c3_mx4_bytes", rows, cols));
+        if (cols < 1) return fail(C3_E_INVALID, "c3_mx4_bytes: cols must be at least 1");
+        if (codes) *codes = codes_bytes(rows, cols);
+        if (scales) *scales = scales_bytes(rows, cols);
+        return C3_OK;
+    })
 }
 
 c3_status c3_mx4_quantize(const void* x, c3_dtype dtype, int64_t rows, int64_t cols, int64_t ld,

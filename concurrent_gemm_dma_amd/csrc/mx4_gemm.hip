@@ -264,7 +264,8 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 // 8192x53248x16384 2.97 ms, 4.8 PFLOP/s; 8192x8192x8192 0.26 ms with the matrix pipe busy 60% of
 // the cycles at 1.72 GHz. Matrix instructions alone, operands in registers and random, run at 6.4
 // PFLOP/s here (power holds the clock near 1.57 GHz; 9.7 on zeros). A tile's start and end cost a
-// CU 12-16 us, which short K shows: 8192 slots of 8 experts x 14336x4096 0.62 ms, 3.1 PFLOP/s.
+// CU 10-14 us (stores 5, their way through LDS 3-4), which short K shows: 16384 slots of 8 experts x
+// 14336x4096 0.61 ms, 3.1 PFLOP/s.
 //
 // No load leaves its array: rows past M or N are clamped to a valid row, stages past the last one
 // load the last one again into a buffer nobody reads, and a scale unit (16 bytes) that would pass
@@ -277,8 +278,8 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 __device__ __forceinline__ i32x4_t rsrc_of(const void* base) {
     const uint64_t a = (uint64_t)(uintptr_t)base;
     i32x4_t w;
-    w.x = (int)(uint32_t)a;
-    w.y = (int)((uint32_t)(a >> 32) & 0xFFFFu);
+    w.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+    w.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu));
     w.z = -1;           // every offset is in range by construction
     w.w = 0x00020000;   // raw buffer, 32-bit data format
     return w;
@@ -542,56 +543,59 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
     }
     __syncthreads();
 
-    // ---- C: 32 rows at a time through LDS (this wave's own 17 KiB), so that it leaves in whole
-    // 128-byte lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each
-    // 32 x 32 block; a row's 16-byte chunks are permuted by its number against bank conflicts.
+    // ---- C: through LDS (this wave's quarter of the stages), so that it leaves in whole 128-byte
+    // lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each 32 x 32
+    // block; a row's 16-byte chunks are permuted by its number against bank conflicts. A slot
+    // without an expert has sums of 0 and weight 0.
     int slot[TM];
     float weight[TM];
 #pragma unroll
     for (int mi = 0; mi < TM; ++mi) slot[mi] = slot_at(g, r.begin + wm * 32 * TM + mi * 32 + row32, r.end);
 #pragma unroll
-    for (int mi = 0; mi < TM; ++mi) weight[mi] = weight_of(g, slot[mi]);
-    char* out = smem + wave * (32 * 32 * TN * 4 + 32 * 4 * TM);
-    int* slots = reinterpret_cast<int*>(out + 32 * 32 * TN * 4);
+    for (int mi = 0; mi < TM; ++mi) weight[mi] = r.expert < g.E ? weight_of(g, slot[mi]) : 0.f;
+    char* out = smem + wave * (SCALES / 4);
+    int* slots = reinterpret_cast<int*>(smem + SCALES) + wave * 32 * TM;
     if (half == 0)
 #pragma unroll
         for (int mi = 0; mi < TM; ++mi) slots[mi * 32 + row32] = slot[mi];
     const int nw = n0 + wn * 32 * TN;
-    auto store = [&](auto f32_c) {
+    auto store = [&](auto f32_c, auto full_c) {
         constexpr bool F32 = decltype(f32_c)::value != 0;
+        constexpr bool FULL = decltype(full_c)::value != 0;  // whole 16-byte pieces only
         constexpr int size = F32 ? 4 : 2, row_bytes = 32 * TN * size, chunks = row_bytes / 16;
+        constexpr int FIT = SCALES / 4 / (32 * row_bytes), PER = FIT < TM ? FIT : TM;  // 32-row blocks at once
         const bool aligned = (((uintptr_t)g.C | (uint64_t)g.ldc * size) & 15) == 0;
 #pragma unroll
-        for (int mi = 0; mi < TM; ++mi) {
+        for (int m0 = 0; m0 < TM; m0 += PER) {
 #pragma unroll
-            for (int ni = 0; ni < TN; ++ni)
+            for (int mi = m0; mi < m0 + PER; ++mi)
 #pragma unroll
-                for (int v = 0; v < 16; v += 4) {
-                    const int n = 32 * ni + 2 * v + 4 * half;
-                    f32x4_t y;
+                for (int ni = 0; ni < TN; ++ni)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[i] = r.expert < g.E ? weight[mi] * acc[mi][ni][v + i] : 0.f;
-                    if constexpr (F32) {
-                        const int c = (n / 4) ^ (row32 & (chunks - 1));
-                        *reinterpret_cast<f32x4_t*>(out + row32 * row_bytes + c * 16) = y;
-                    } else {
-                        const int c = (n / 8) ^ (row32 & (chunks - 1));
-                        bf16x4_t b = {static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
-                                      static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
-                        *reinterpret_cast<bf16x4_t*>(out + row32 * row_bytes + c * 16 + (n & 4) * 2) = b;
+                    for (int v = 0; v < 16; v += 4) {
+                        const int n = 32 * ni + 2 * v + 4 * half;
+                        char* row = out + ((mi - m0) * 32 + row32) * row_bytes;
+                        f32x4_t y;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] = weight[mi] * acc[mi][ni][v + i];
+                        if constexpr (F32) {
+                            *reinterpret_cast<f32x4_t*>(row + ((n / 4) ^ (row32 & (chunks - 1))) * 16) = y;
+                        } else {
+                            bf16x4_t b = {static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
+                                          static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
+                            *reinterpret_cast<bf16x4_t*>(row + ((n / 8) ^ (row32 & (chunks - 1))) * 16 + (n & 4) * 2) = b;
+                        }
                     }
-                }
             own_lds_fence();
-            constexpr int EACH = chunks / 2;  // of a lane
 #pragma unroll
-            for (int u = 0; u < EACH; ++u) {
-                const int i = u * 64 + lane, m = i / chunks, c = i % chunks, s = slots[mi * 32 + m];
+            for (int u = 0; u < PER * chunks / 2; ++u) {
+                const int i = u * 64 + lane, m = i / chunks, c = i % chunks, s = slots[m0 * 32 + m];
                 const int n = nw + c * (16 / size);
-                if (s < 0 || n >= g.N) continue;
+                if (s < 0 || (!FULL && n >= g.N)) continue;
                 const i32x4_t v = *reinterpret_cast<const i32x4_t*>(out + m * row_bytes + (c ^ (m & (chunks - 1))) * 16);
                 char* p = static_cast<char*>(g.C) + ((size_t)s * g.ldc + n) * size;
                 const int fit = (g.N - n) * size;
-                if (fit >= 16 && aligned) {
+                if (FULL || (fit >= 16 && aligned)) {
                     *reinterpret_cast<i32x4_t*>(p) = v;
                 } else if (fit >= 16) {
                     __builtin_memcpy(__builtin_assume_aligned(p, 2), &v, 16);
@@ -608,8 +612,15 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
             own_lds_fence();
         }
     };
-    if (g.f32) store(Int<1>{});
-    else store(Int<0>{});
+    const int bytes = g.f32 ? 4 : 2;
+    const bool full = nw + 32 * TN <= g.N && (((uintptr_t)g.C | (uint64_t)g.ldc * bytes) & 15) == 0;
+    if (g.f32) {
+        if (full) store(Int<1>{}, Int<1>{});
+        else store(Int<1>{}, Int<0>{});
+    } else {
+        if (full) store(Int<0>{}, Int<1>{});
+        else store(Int<0>{}, Int<0>{});
+    }
 }
 
 // Most tiles of `bm` rows that the order can need.
@@ -629,8 +640,9 @@ double tiles_of(const c3::Mx4Gemm& g, int bm) {
 // Rows of the tile to use: 16, 32 (mx4_gemm_rows) or 128, 256 (mx4_gemm_tile). Up to 16 rows (8 of
 // an expert on average, since loads are uneven) the weights' bytes decide, and the smallest tile
 // keeps the most of them in flight. Past that, the least time in us of a model fitted to measured
-// times: a chunk (32 x 32 x 512) of mx4_gemm_rows takes a CU 0.55; a round of tiles takes a fixed
-// part and, per 128 columns, between `low` and `high` with the share of the device that it fills.
+// times: mx4_gemm_rows takes a CU 0.55 for a chunk (32 x 32 x 512) and 0.18 for a tile; a round of
+// the others takes a fixed part and, per 128 columns, between `low` and `high` with the share of
+// the device that it fills.
 // Measured: 64 rows x 2048x8192 13 us in tiles of 32 against 19 of 128, x 28672x8192 70 against 37;
 // 1024x4096x4096 15 us in tiles of 128 against 34 of 256.
 int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
@@ -644,7 +656,7 @@ int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
     };
     const double t256 = rounds(tiles(256), n_cu, 16.0, 0.4, 0.77);
     const double t128 = rounds(tiles(128), 2 * n_cu, g.order ? 8.0 : 5.0, 0.16, 0.7);
-    const double t32 = 4.0 + std::ceil(tiles(32) * nk / 4 / n_cu) * 0.55;
+    const double t32 = 4.0 + std::ceil(tiles(32) * nk / 4 / n_cu) * 0.55 + tiles(32) / n_cu * 0.18;
     return t32 < std::min(t128, t256) ? 32 : t256 < t128 ? 256 : 128;
 }
 
