@@ -219,6 +219,13 @@ def test_route_backward(c3gpu, T, E, k, kind, renorm, dtype):
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k,dtype", [(4100, 17, 3, 0), (4101, 100, 8, 1), (4099, 201, 16, 0)])
+def test_route_backward_large_batches(c3gpu, T, E, k, kind, renorm, dtype):
+    test_route_backward(c3gpu, T, E, k, kind, renorm, dtype)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
 def test_route_backward_against_differences(c3gpu, kind, renorm):
     """dlogits . v is the slope of the forward's weights along v."""
     rng = np.random.default_rng(11)
