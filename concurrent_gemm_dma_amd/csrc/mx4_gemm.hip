@@ -40,9 +40,35 @@ struct Rows {
     int begin, end, expert;
 };
 
+// What 64 experts, one a lane, own of the order, in tiles of BM positions. Offsets are clamped to the
+// order's range, so whatever they hold no position outside it is read.
+template <int BM>
+struct Share {
+    int lo = 0, hi = 0, tiles, sum, total;  // sum: of the tiles up to this lane's
+    __device__ __forceinline__ Share(const Args& g, int e) {
+        if (e <= g.E) {
+            lo = min(max(g.offsets[e], 0), g.M);
+            hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.M) : g.M;
+        }
+        tiles = sum = (hi - lo + BM - 1) / BM;
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(sum, d);
+            if (lane >= d) sum += up;
+        }
+        total = __builtin_amdgcn_readlane(sum, 63);
+    }
+    // tile t < total of these, the first expert being e0
+    __device__ __forceinline__ Rows pick(int t, int e0) const {
+        const int f = __builtin_ctzll(__ballot(sum > t));
+        const int begin = __builtin_amdgcn_readlane(lo, f) + (t - __builtin_amdgcn_readlane(sum - tiles, f)) * BM;
+        return {begin, min(__builtin_amdgcn_readlane(hi, f), begin + BM), e0 + f};
+    }
+};
+
 // Tile t of BM positions, counted over the experts in turn, each expert's range cut into tiles of
-// its own. Every wave looks at 64 experts at a time. false past the last tile. Offsets are clamped
-// to the order's range, so whatever they hold no position outside it is read.
+// its own. false past the last tile.
 template <int BM>
 __device__ __forceinline__ bool find_rows(const Args& g, int t, Rows& r) {
     if (!g.order) {
@@ -52,36 +78,23 @@ __device__ __forceinline__ bool find_rows(const Args& g, int t, Rows& r) {
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int e0 = 0; e0 <= g.E; e0 += 64) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e <= g.E) {
-            lo = min(max(g.offsets[e], 0), g.M);
-            hi = e < g.E ? min(max(g.offsets[e + 1], lo), g.M) : g.M;
-        }
-        const int tiles = (hi - lo + BM - 1) / BM;
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
-        const int total = __shfl(sum, 63);
-        if (t < base + total) {
-            const uint64_t past = __ballot(base + sum > t);
-            const int f = __builtin_ctzll(past);
-            const int first = base + __shfl(sum - tiles, f);
-            r.begin = __shfl(lo, f) + (t - first) * BM;
-            r.end = min(__shfl(hi, f), r.begin + BM);
-            r.expert = e0 + f;
+        const Share<BM> s(g, e0 + lane);
+        if (t < base + s.total) {
+            r = s.pick(t - base, e0);
             return true;
         }
-        base += total;
+        base += s.total;
     }
     return false;
 }
 
-// All tiles of BM positions of the order, the slots without an expert among them; no more than
-// the grid was made for, whatever the offsets hold.
+// No more tiles than the grid was made for, whatever the offsets hold.
+template <int BM>
+__device__ __forceinline__ int most_tiles(const Args& g) {
+    return g.M / BM + min(g.E + 1, g.M);
+}
+
+// All tiles of BM positions of the order, the slots without an expert among them.
 template <int BM>
 __device__ __forceinline__ int count_tiles(const Args& g) {
     const int lane = threadIdx.x & 63;
@@ -93,7 +106,7 @@ __device__ __forceinline__ int count_tiles(const Args& g) {
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
-    return min(__builtin_amdgcn_readfirstlane(n), g.M / BM + min(g.E + 1, g.M));
+    return min(__builtin_amdgcn_readfirstlane(n), most_tiles<BM>(g));
 }
 
 // Row of A and of C, and the weight, of one position (slot -1: not a slot; nothing is stored).
@@ -347,17 +360,37 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int tiles_n = (g.N + BN - 1) / BN;
-    const int tiles_m = g.order ? count_tiles<BM>(g) : (g.M + BM - 1) / BM;
-    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
     int tm, tn;
-    map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
     Rows r;
-    if (!find_rows<BM>(g, tm, r)) return;
+    if (g.order && g.E < 64) {  // one look at the offsets gives both
+        const Share<BM> s(g, lane);
+        const int tiles_m = min(s.total, most_tiles<BM>(g));
+        if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+        map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        r = s.pick(__builtin_amdgcn_readfirstlane(tm), 0);
+    } else {
+        const int tiles_m = g.order ? count_tiles<BM>(g) : (g.M + BM - 1) / BM;
+        if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+        map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        if (!find_rows<BM>(g, tm, r)) return;
+    }
     r.begin = __builtin_amdgcn_readfirstlane(r.begin);
     r.end = __builtin_amdgcn_readfirstlane(r.end);
     r.expert = __builtin_amdgcn_readfirstlane(r.expert);
     const int n0 = tn * BN;
     const int half = lane >> 5, row32 = lane & 31;
+
+    // slots and weights of this lane's rows of C: read ahead where registers are left
+    constexpr bool EARLY = NM < 16;
+    int slot[TM];
+    float weight[TM];
+    auto rows_of_c = [&] {
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) slot[mi] = slot_at(g, r.begin + wm * 32 * TM + mi * 32 + row32, r.end);
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) weight[mi] = r.expert < g.E ? weight_of(g, slot[mi]) : 0.f;
+    };
+    if (EARLY) rows_of_c();
 
     f32x16_t acc[TM][TN];
 #pragma unroll
@@ -547,12 +580,7 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void mx4_ge
     // lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each 32 x 32
     // block; a row's 16-byte chunks are permuted by its number against bank conflicts. A slot
     // without an expert has sums of 0 and weight 0.
-    int slot[TM];
-    float weight[TM];
-#pragma unroll
-    for (int mi = 0; mi < TM; ++mi) slot[mi] = slot_at(g, r.begin + wm * 32 * TM + mi * 32 + row32, r.end);
-#pragma unroll
-    for (int mi = 0; mi < TM; ++mi) weight[mi] = r.expert < g.E ? weight_of(g, slot[mi]) : 0.f;
+    if (!EARLY) rows_of_c();
     char* out = smem + wave * (SCALES / 4);
     int* slots = reinterpret_cast<int*>(smem + SCALES) + wave * 32 * TM;
     if (half == 0)
