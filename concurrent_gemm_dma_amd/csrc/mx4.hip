@@ -9,6 +9,7 @@
 // 8192x16384 bf16: quantise 54 us (6.2 TB/s, the rate of a large copy), dequantise 47 us; one row of
 // 16384 2.2 us each, a launch.
 #include "c3_internal.h"
+#include "pieces.h"
 
 #include <type_traits>
 
@@ -121,22 +122,11 @@ __device__ __forceinline__ Eight<BF16> load_eight(const char* p, int64_t fit) {
     return x;
 }
 
-// Row and piece of a lane: lane `tid` of a workgroup that starts at piece `first` (counted over
-// all rows of `per_row` pieces). The division is the workgroup's; a lane's part is below
-// per_row + 1024, where multiplying by ceil(2^32 / per_row) is exact up to 2^11 pieces a row, and
-// past that a row ends at most once.
-struct At {
-    int64_t row;
-    uint32_t piece;
-};
-__device__ __forceinline__ At locate(int64_t first, uint32_t tid, uint32_t per_row, uint32_t magic) {
-    const int64_t row = first / per_row;
-    const uint32_t x = (uint32_t)(first - row * per_row) + tid;
-    const uint32_t q = per_row > 2048 ? (uint32_t)(x >= per_row) : __umulhi(x, magic);
-    return {row + q, x - q * per_row};
-}
 constexpr int kThreads = 256;
 constexpr int kPieces = 2;  // of a lane, 256 lanes apart
+static_assert(kThreads * kPieces <= 512, "lanes that locate takes");
+using c3::At;
+using c3::locate;
 
 // Four lanes quantise a block, eight values each.
 template <bool BF16>
@@ -328,8 +318,6 @@ __global__ __launch_bounds__(kThreads) void dequantize_rows(const void* __restri
         }
     }
 }
-
-uint32_t magic_of(uint32_t per_row) { return (uint32_t)(((uint64_t(1) << 32) + per_row - 1) / per_row); }
 
 }  // namespace
 

@@ -377,3 +377,28 @@ def test_experts_never_follow_bad_plans(c3gpu):
                               K, N)
     torch.cuda.synchronize()
     assert (C[-1] == -7.0).all().item()
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("cols", [1, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("rows", [2, 513, 1500])
+def test_dequantise_narrow(c3gpu, rows, cols, dtype):
+    """Few columns and many rows: one lane or a few hold a row, over several workgroups."""
+    test_dequantise(c3gpu, rows, cols, cols + 3, dtype)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("tokens", range(1, 10))
+def test_quantise_transposed_read_back(c3gpu, tokens, dtype):
+    """A few tokens quantised along the tokens: the operand's rows are the features, its columns few."""
+    import torch
+
+    features = 700
+    x = wide(np.random.default_rng(tokens), (tokens, features))
+    codes, scales = quantise(c3gpu, x, dtype, False, True)
+    y = filled((features + 1, tokens), 1)
+    c3gpu.c3_mx4_dequantize(dev(codes), dev(scales), features, tokens, y, 1, tokens)
+    torch.cuda.synchronize()
+    want = ref.values(*ref.quantize(np.ascontiguousarray(x.T)), tokens).astype(np.float32)
+    np.testing.assert_array_equal(y[:features].cpu().numpy(), want)
+    assert (y[features] == -7.0).all().item()
