@@ -1,8 +1,10 @@
 // layer.cpp -- the extern "C" entry points of expert layers (routing, MX FP4 operands and their
 // products) declared in include/c3.h: every argument is checked before any launch.
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <map>
+#include <utility>
 
 #include "c3_internal.h"
 
@@ -90,15 +92,24 @@ c3_status check_route(const char* who, const RouteArgs& a, const c3_route_opts* 
     return C3_OK;
 }
 
-std::map<hipStream_t, void*>& plan_workspaces() {
-    static std::map<hipStream_t, void*> w;
+// hipStreamPerThread is one handle for a stream in each host thread.
+using StreamKey = std::pair<hipStream_t, uint64_t>;
+
+StreamKey stream_key(hipStream_t stream) {
+    static std::atomic<uint64_t> threads{0};
+    thread_local const uint64_t thread = ++threads;
+    return {stream, stream == hipStreamPerThread ? thread : 0};
+}
+
+std::map<StreamKey, void*>& plan_workspaces() {
+    static std::map<StreamKey, void*> w;
     return w;
 }
 
 // The plan workspace of `stream`, allocated on first need. Its size is fixed, so it never moves
 // while a captured graph may hold its address.
 c3_status plan_workspace(hipStream_t stream, void** out) {
-    auto it = plan_workspaces().find(stream);
+    auto it = plan_workspaces().find(stream_key(stream));
     if (it == plan_workspaces().end()) {
         hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
         C3_HIP_TRY(hipStreamIsCapturing(stream, &capture));
@@ -108,7 +119,7 @@ c3_status plan_workspace(hipStream_t stream, void** out) {
                         "workspace; make one before capturing the stream");
         void* p = nullptr;
         C3_HIP_TRY(hipMalloc(&p, C3_PLAN_WORKSPACE_BYTES));
-        it = plan_workspaces().emplace(stream, p).first;
+        it = plan_workspaces().emplace(stream_key(stream), p).first;
     }
     *out = it->second;
     return C3_OK;

@@ -328,3 +328,45 @@ def test_route_in_a_captured_graph(c3gpu):
                                    (262145, 64, 1), (40000, 1024, 8)])
 def test_plan_at_the_borders_of_its_kernels(c3gpu, T, E, k):
     test_plan(c3gpu, T, E, k)
+
+
+def large_plan(seed, T=20000, E=100, k=3):
+    """(idx, buffers, want) of a plan above 4096 slots, on the device."""
+    import torch
+
+    idx = np.random.default_rng(seed).integers(-1, E, (T, k)).astype(np.int32)
+    whole = lambda n: torch.full((n,), -9, dtype=torch.int32, device="cuda:0")  # noqa: E731
+    return dev(idx), (whole(T * k), whole(E + 1)), ref.plan(idx, E), (T, k, E)
+
+
+def planned(buffers, want):
+    return all((b.cpu().numpy() == w).all() for b, w in zip(buffers, want))
+
+
+def test_plan_on_the_per_thread_stream(c3gpu):
+    """One handle, a stream of its own in each host thread: the plans may overlap."""
+    import threading
+
+    import torch
+
+    per_thread = 2  # hipStreamPerThread
+    work = [[large_plan(10 * t + i) for i in range(6)] for t in range(4)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def plan(mine):
+        try:
+            for _ in range(5):
+                for idx, buffers, _, size in mine:
+                    c3gpu.c3_route_plan(idx, *size, *buffers, per_thread)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=plan, args=(mine,)) for mine in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    assert all(planned(buffers, want) for mine in work for _, buffers, want, _ in mine)
