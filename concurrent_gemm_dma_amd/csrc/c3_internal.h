@@ -160,7 +160,7 @@ struct RouteArgs {
 };
 c3_status route_enqueue(const RouteArgs& a, hipStream_t stream);
 c3_status route_backward_enqueue(const RouteArgs& a, hipStream_t stream);
-// `workspace`: C3_PLAN_WORKSPACE_BYTES, needed where plan_needs_workspace says so.
+// `workspace`: half of C3_PLAN_WORKSPACE_BYTES, needed where plan_needs_workspace says so.
 bool plan_needs_workspace(int64_t slots);
 c3_status plan_enqueue(const int32_t* idx, int64_t T, int top_k, int E, int32_t* order,
                        int32_t* offsets, void* workspace, hipStream_t stream);

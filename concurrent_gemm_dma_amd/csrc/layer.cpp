@@ -106,14 +106,18 @@ std::map<StreamKey, void*>& plan_workspaces() {
     return w;
 }
 
-// The plan workspace of `stream`, allocated on first need. Its size is fixed, so it never moves
-// while a captured graph may hold its address.
+// What a plan on `stream` works in, allocated on first need: the first half for eager calls, the
+// second for captured ones, so that a replay elsewhere and an eager call on the stream it was
+// captured on may overlap. Its size is fixed, so it never moves while a captured graph may hold its
+// address.
 c3_status plan_workspace(hipStream_t stream, void** out) {
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (stream && stream != hipStreamLegacy)  // the null stream is never captured
+        C3_HIP_TRY(hipStreamIsCapturing(stream, &capture));
+    const bool capturing = capture != hipStreamCaptureStatusNone;
     auto it = plan_workspaces().find(stream_key(stream));
     if (it == plan_workspaces().end()) {
-        hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
-        C3_HIP_TRY(hipStreamIsCapturing(stream, &capture));
-        if (capture != hipStreamCaptureStatusNone)
+        if (capturing)
             return fail(C3_E_UNSUPPORTED,
                         "c3_route_plan: the first call above 4096 slots on a stream allocates its "
                         "workspace; make one before capturing the stream");
@@ -121,7 +125,7 @@ c3_status plan_workspace(hipStream_t stream, void** out) {
         C3_HIP_TRY(hipMalloc(&p, C3_PLAN_WORKSPACE_BYTES));
         it = plan_workspaces().emplace(stream_key(stream), p).first;
     }
-    *out = it->second;
+    *out = static_cast<char*>(it->second) + (capturing ? C3_PLAN_WORKSPACE_BYTES / 2 : 0);
     return C3_OK;
 }
 

@@ -442,7 +442,7 @@ __global__ __launch_bounds__(256) void route_gradient(const T* __restrict__ logi
 constexpr int kPlanWaves = 16, kPlanThreads = 64 * kPlanWaves;
 constexpr int kMaxGroups = 128;
 constexpr int kMaxBins = C3_MAX_EXPERTS + 1;  // the last one in use: slots without an expert
-static_assert((size_t)kMaxGroups * kMaxBins * 4 <= C3_PLAN_WORKSPACE_BYTES, "plan workspace");
+static_assert((size_t)kMaxGroups * kMaxBins * 4 <= C3_PLAN_WORKSPACE_BYTES / 2, "plan workspace");
 constexpr int64_t kOneGroup = 4096;  // slots that one workgroup lays out by itself
 constexpr int kFew = 64;
 

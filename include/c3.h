@@ -437,8 +437,8 @@ c3_status c3_route_backward(const void* logits, c3_dtype dtype, int64_t n_tokens
  * Above 4096 slots the call needs C3_PLAN_WORKSPACE_BYTES of device memory, which the library
  * allocates per stream on first need (hipStreamPerThread: per host thread) and keeps until
  * c3_finalize; on a stream that is being captured into a graph that first need is refused
- * (C3_E_UNSUPPORTED): plan once before. Graphs captured on one stream share its workspace: their
- * replays must not overlap in time. */
+ * (C3_E_UNSUPPORTED): plan once before. Eager calls and captured ones work in halves of their own.
+ * Graphs captured on one stream share a half: their replays must not overlap in time. */
 #define C3_PLAN_WORKSPACE_BYTES (2u << 20)
 c3_status c3_route_plan(const int32_t* idx, int64_t n_tokens, int top_k, int n_experts,
                         int32_t* order, int32_t* offsets, void* stream);

@@ -370,3 +370,29 @@ def test_plan_on_the_per_thread_stream(c3gpu):
     torch.cuda.synchronize()
     assert not failed
     assert all(planned(buffers, want) for mine in work for _, buffers, want, _ in mine)
+
+
+def test_plan_beside_the_replay_of_a_graph(c3gpu):
+    """Eager plans on the stream a graph was captured on, while it is replayed on another."""
+    import torch
+
+    stream, other = torch.cuda.Stream(), torch.cuda.Stream()
+    idx, buffers, want, size = large_plan(1)
+    e_idx, e_buffers, e_want, _ = large_plan(2)
+    torch.cuda.synchronize()
+    c3gpu.c3_route_plan(idx, *size, *buffers, stream)  # the workspace
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(20):
+            c3gpu.c3_route_plan(idx, *size, *buffers, stream)
+    for _ in range(4):
+        for b in buffers + e_buffers:
+            b.fill_(-9)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            graph.replay()
+        for _ in range(20):
+            c3gpu.c3_route_plan(e_idx, *size, *e_buffers, stream)
+        torch.cuda.synchronize()
+        assert planned(buffers, want) and planned(e_buffers, e_want)
