@@ -194,6 +194,8 @@ struct Mx4Gemm {
     int64_t a_rows = 0;
 };
 c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream);
+// A stream that the library is about to destroy: its workspace is free for another one.
+void layer_forget_stream(hipStream_t stream);
 void layer_release_workspaces();
 
 // ---- SDMA (sdma.cpp) ----------------------------------------------------------------------------

@@ -135,6 +135,7 @@ c3_status user_stream_destroy(hipStream_t s) {
     auto& us = user_streams();
     if (!us.count(s)) return fail(C3_E_INVALID, "stream %p was not created by c3_stream_create", (void*)s);
     us.erase(s);
+    layer_forget_stream(s);
     C3_HIP_TRY(hipStreamDestroy(s));
     return C3_OK;
 }

@@ -92,6 +92,12 @@ c3_status check_route(const char* who, const RouteArgs& a, const c3_route_opts* 
     return C3_OK;
 }
 
+// The plan workspace of a stream: the first half for eager calls, the second for captured ones, so
+// that a replay elsewhere and an eager call on the stream it was captured on may overlap.
+struct PlanWorkspace {
+    char* p = nullptr;
+    bool captured = false;  // a graph may hold the second half
+};
 // hipStreamPerThread is one handle for a stream in each host thread.
 using StreamKey = std::pair<hipStream_t, uint64_t>;
 
@@ -101,31 +107,47 @@ StreamKey stream_key(hipStream_t stream) {
     return {stream, stream == hipStreamPerThread ? thread : 0};
 }
 
-std::map<StreamKey, void*>& plan_workspaces() {
-    static std::map<StreamKey, void*> w;
+std::map<StreamKey, PlanWorkspace>& plan_workspaces() {
+    static std::map<StreamKey, PlanWorkspace> w;
+    return w;
+}
+// Workspaces of destroyed streams: free to take, and held by graphs until the end.
+std::vector<char*>& spare_workspaces() {
+    static std::vector<char*> w;
+    return w;
+}
+std::vector<char*>& held_workspaces() {
+    static std::vector<char*> w;
     return w;
 }
 
-// What a plan on `stream` works in, allocated on first need: the first half for eager calls, the
-// second for captured ones, so that a replay elsewhere and an eager call on the stream it was
-// captured on may overlap. Its size is fixed, so it never moves while a captured graph may hold its
-// address.
+// What a plan on `stream` works in, allocated on first need. Its size is fixed, so it never moves
+// while a captured graph may hold its address.
 c3_status plan_workspace(hipStream_t stream, void** out) {
     hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
     if (stream && stream != hipStreamLegacy)  // the null stream is never captured
         C3_HIP_TRY(hipStreamIsCapturing(stream, &capture));
     const bool capturing = capture != hipStreamCaptureStatusNone;
-    auto it = plan_workspaces().find(stream_key(stream));
-    if (it == plan_workspaces().end()) {
+    auto& all = plan_workspaces();
+    auto it = all.find(stream_key(stream));
+    if (it == all.end()) {
         if (capturing)
             return fail(C3_E_UNSUPPORTED,
                         "c3_route_plan: the first call above 4096 slots on a stream allocates its "
                         "workspace; make one before capturing the stream");
-        void* p = nullptr;
-        C3_HIP_TRY(hipMalloc(&p, C3_PLAN_WORKSPACE_BYTES));
-        it = plan_workspaces().emplace(stream_key(stream), p).first;
+        PlanWorkspace w;
+        if (!spare_workspaces().empty()) {
+            w.p = spare_workspaces().back();
+            spare_workspaces().pop_back();
+        } else {
+            void* p = nullptr;
+            C3_HIP_TRY(hipMalloc(&p, C3_PLAN_WORKSPACE_BYTES));
+            w.p = static_cast<char*>(p);
+        }
+        it = all.emplace(stream_key(stream), w).first;
     }
-    *out = static_cast<char*>(it->second) + (capturing ? C3_PLAN_WORKSPACE_BYTES / 2 : 0);
+    it->second.captured |= capturing;
+    *out = it->second.p + (capturing ? C3_PLAN_WORKSPACE_BYTES / 2 : 0);
     return C3_OK;
 }
 
@@ -141,9 +163,22 @@ size_t scales_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (mx4_pad
 
 }  // namespace
 
+void layer_forget_stream(hipStream_t stream) {
+    auto& all = plan_workspaces();
+    auto it = all.find(stream_key(stream));
+    if (it == all.end()) return;
+    const bool idle = !it->second.captured && hipStreamSynchronize(stream) == hipSuccess;
+    (idle ? spare_workspaces() : held_workspaces()).push_back(it->second.p);
+    all.erase(it);
+}
+
 void layer_release_workspaces() {
-    for (auto& kv : plan_workspaces()) (void)hipFree(kv.second);
+    for (auto& kv : plan_workspaces()) (void)hipFree(kv.second.p);
     plan_workspaces().clear();
+    for (auto* list : {&spare_workspaces(), &held_workspaces()}) {
+        for (char* p : *list) (void)hipFree(p);
+        list->clear();
+    }
 }
 
 }  // namespace c3

@@ -436,9 +436,11 @@ c3_status c3_route_backward(const void* logits, c3_dtype dtype, int64_t n_tokens
  * offsets[e+1]). n_tokens = 0 gives offsets of 0. n_tokens * top_k < 2^31.
  * Above 4096 slots the call needs C3_PLAN_WORKSPACE_BYTES of device memory, which the library
  * allocates per stream on first need (hipStreamPerThread: per host thread) and keeps until
- * c3_finalize; on a stream that is being captured into a graph that first need is refused
- * (C3_E_UNSUPPORTED): plan once before. Eager calls and captured ones work in halves of their own.
- * Graphs captured on one stream share a half: their replays must not overlap in time. */
+ * c3_stream_destroy or c3_finalize; on a stream that is being captured into a graph that first
+ * need is refused (C3_E_UNSUPPORTED): plan once before. Eager calls and captured ones work in
+ * halves of their own. Graphs captured on one stream share a half, which lasts until c3_finalize:
+ * their replays must not overlap in time. A stream that planned and is destroyed by other means
+ * than c3_stream_destroy has to be idle then. */
 #define C3_PLAN_WORKSPACE_BYTES (2u << 20)
 c3_status c3_route_plan(const int32_t* idx, int64_t n_tokens, int top_k, int n_experts,
                         int32_t* order, int32_t* offsets, void* stream);

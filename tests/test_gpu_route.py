@@ -396,3 +396,27 @@ def test_plan_beside_the_replay_of_a_graph(c3gpu):
             c3gpu.c3_route_plan(e_idx, *size, *e_buffers, stream)
         torch.cuda.synchronize()
         assert planned(buffers, want) and planned(e_buffers, e_want)
+
+
+def test_destroyed_streams_give_their_plan_workspace_back(c3gpu):
+    import torch
+
+    idx, buffers, want, size = large_plan(3)
+    torch.cuda.synchronize()
+
+    def taken(n, plan):
+        """Device memory that n streams leave behind."""
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        for _ in range(n):
+            s = c3gpu.c3_stream_create()
+            if plan:
+                c3gpu.c3_route_plan(idx, *size, *buffers, s)
+            c3gpu.c3_stream_destroy(s)
+        torch.cuda.synchronize()
+        return free - torch.cuda.mem_get_info()[0]
+
+    taken(1, True)
+    streams = taken(20, False)
+    assert taken(20, True) - streams < 10 * c3gpu.C3_PLAN_WORKSPACE_BYTES
+    assert planned(buffers, want)
