@@ -688,18 +688,19 @@ int choose_tile(const c3::Mx4Gemm& g, int P, int n_cu) {
     return t32 < std::min(t128, t256) ? 32 : t256 < t128 ? 256 : 128;
 }
 
+// false: more workgroups than one launch takes (2^32 threads).
 template <int MT, int NT>
-c3_status launch_rows(const c3::Mx4Gemm& g, const Args& a, int n_cu, hipStream_t stream) {
+bool launch_rows(const c3::Mx4Gemm& g, const Args& a, int n_cu, hipStream_t stream) {
     const int64_t groups = most_tiles(g, 16 * MT) * ((g.N + 16 * NT - 1) / (16 * NT));
-    if (groups >= (1 << 22)) return c3::fail(C3_E_INVALID, "MX FP4 product: too many tiles");
     // As many waves as fit the device at one time (24 a CU) with two chunks of K each at least, so
     // that no second round of workgroups has part of the device to itself.
     int waves = 1;
     while (waves < (MT * NT == 4 ? 16 : 8) && 2 * waves * groups <= 24 * (int64_t)n_cu && waves * 1024 < a.P)
         waves *= 2;
+    if (groups * 64 * waves >= (int64_t(1) << 32)) return false;
     hipLaunchKernelGGL((mx4_gemm_rows<MT, NT>), dim3((unsigned)groups), dim3(64 * waves),
                        waves * 256 * MT * NT * sizeof(float), stream, a);
-    return C3_OK;
+    return true;
 }
 
 }  // namespace
@@ -711,18 +712,18 @@ c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream) {
                     g.M, g.N, (int)mx4_padded(g.K), g.T, g.top_k, g.order ? g.E : 1,
                     (int)g.a_rows, (int)(g.dtype == C3_F32)};
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
-    const int tile = choose_tile(g, a.P, n_cu);
+    int tile = choose_tile(g, a.P, n_cu);
+    if (tile == 32 && !launch_rows<2, 2>(g, a, n_cu, stream)) tile = 128;
+    if (tile == 16 && !launch_rows<1, 2>(g, a, n_cu, stream)) tile = 128;
     if (tile >= 128) {
-        const int64_t groups = most_tiles(g, tile) * ((g.N + tile - 1) / tile);
+        auto groups_of = [&](int bm) { return most_tiles(g, bm) * ((g.N + bm - 1) / bm); };
+        if (groups_of(tile) >= (1 << 24)) tile = 256;  // one launch takes 2^32 threads
+        const int64_t groups = groups_of(tile);
         if (groups >= (1 << 24)) return fail(C3_E_INVALID, "MX FP4 product: too many tiles");
         // 128 rows: four stages in LDS where that costs no CU its second workgroup
         auto kernel = tile == 256 ? mx4_gemm_tile<4, 4, 2>
                       : tiles_of(g, 128) <= n_cu ? mx4_gemm_tile<2, 2, 4> : mx4_gemm_tile<2, 2, 2>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(256), 0, stream, a);
-    } else if (tile == 32) {
-        C3_TRY((launch_rows<2, 2>(g, a, n_cu, stream)));
-    } else {
-        C3_TRY((launch_rows<1, 2>(g, a, n_cu, stream)));
     }
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;

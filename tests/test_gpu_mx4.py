@@ -402,3 +402,25 @@ def test_quantise_transposed_read_back(c3gpu, tokens, dtype):
     want = ref.values(*ref.quantize(np.ascontiguousarray(x.T)), tokens).astype(np.float32)
     np.testing.assert_array_equal(y[:features].cpu().numpy(), want)
     assert (y[features] == -7.0).all().item()
+
+
+def test_experts_wide(c3gpu):
+    """More workgroups than 2^22: 64 experts' rows of 1.4 million columns, on columns spread over them."""
+    import torch
+
+    rng = np.random.default_rng(12)
+    T, E, k, N, K = 64, 64, 8, 1_400_000, 256
+    idx, order, offsets = plan_of(rng, T, E, k, 0.0, 0.0)
+    a, sa, A = operand(rng, T, K)
+    b = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda:0")
+    sb = torch.randint(118, 124, (E, N, K // 32), dtype=torch.uint8, device="cuda:0")
+    C = filled((T * k, N), 0, float("nan"))
+    c3gpu.c3_mx4_gemm_experts(dev(a), dev(sa), T, b, sb, dev(order), dev(offsets), None, C, 0, T, k, E, N, K, N)
+    torch.cuda.synchronize()
+    assert not C.isnan().any().item()
+    some = dev(np.concatenate([np.arange(40), rng.integers(0, N, 200), np.arange(N - 40, N)]))
+    B = ref.values(b[:, some].cpu().numpy(), sb[:, some].cpu().numpy(), K)
+    want, bound = experts_want(A, B, idx, order, offsets, None, T)
+    close(C[:, some].double().cpu().numpy(), want, bound, 0)
+    del b, sb, C
+    torch.cuda.empty_cache()
