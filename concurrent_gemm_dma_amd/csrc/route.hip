@@ -643,10 +643,28 @@ void gradient(const c3::RouteArgs& a, hipStream_t stream) {
 
 namespace c3 {
 
+// One launch takes 2^32 threads, of which a token has up to 64: `launch` with up to 2^25 tokens at a
+// time.
+template <typename Launch>
+static c3_status in_parts(const RouteArgs& a, Launch launch) {
+    constexpr int64_t most = int64_t(1) << 25;
+    const size_t size = a.dtype == C3_BF16 ? 2 : 4;
+    for (int64_t t = 0; t < a.T; t += most) {
+        RouteArgs p = a;
+        p.T = std::min(most, a.T - t);
+        p.logits = static_cast<const char*>(a.logits) + t * a.ld * size;
+        p.idx = a.idx + t * a.o.top_k;
+        if (a.weights) p.weights = a.weights + t * a.o.top_k;
+        if (a.dweights) p.dweights = a.dweights + t * a.o.top_k;
+        if (a.dlogits) p.dlogits = static_cast<char*>(a.dlogits) + t * a.ld_d * size;
+        launch(p);
+        C3_HIP_TRY(hipGetLastError());
+    }
+    return C3_OK;
+}
+
 c3_status route_enqueue(const RouteArgs& a, hipStream_t stream) {
-    if ((a.T + 3) / 4 >= (1 << 24)) return fail(C3_E_INVALID, "c3_route: too many tokens for one launch");
     Choice c;
-    c.n_tokens = a.T;
     c.ld = a.ld;
     c.E = a.E;
     c.k = a.o.top_k;
@@ -659,19 +677,18 @@ c3_status route_enqueue(const RouteArgs& a, hipStream_t stream) {
     c.sigmoid = a.o.score == C3_SCORE_SIGMOID;
     c.renormalize = a.o.renormalize;
     c.scale = a.o.scale;
-    if (a.dtype == C3_BF16) choose<__bf16>(a, c, stream);
-    else choose<float>(a, c, stream);
-    C3_HIP_TRY(hipGetLastError());
-    return C3_OK;
+    return in_parts(a, [&](const RouteArgs& p) {
+        c.n_tokens = p.T;
+        if (a.dtype == C3_BF16) choose<__bf16>(p, c, stream);
+        else choose<float>(p, c, stream);
+    });
 }
 
 c3_status route_backward_enqueue(const RouteArgs& a, hipStream_t stream) {
-    if ((a.T + 3) / 4 >= (1 << 24))
-        return fail(C3_E_INVALID, "c3_route_backward: too many tokens for one launch");
-    if (a.dtype == C3_BF16) gradient<__bf16>(a, stream);
-    else gradient<float>(a, stream);
-    C3_HIP_TRY(hipGetLastError());
-    return C3_OK;
+    return in_parts(a, [&](const RouteArgs& p) {
+        if (a.dtype == C3_BF16) gradient<__bf16>(p, stream);
+        else gradient<float>(p, stream);
+    });
 }
 
 bool plan_needs_workspace(int64_t slots) { return slots > kOneGroup; }

@@ -420,3 +420,36 @@ def test_destroyed_streams_give_their_plan_workspace_back(c3gpu):
     streams = taken(20, False)
     assert taken(20, True) - streams < 10 * c3gpu.C3_PLAN_WORKSPACE_BYTES
     assert planned(buffers, want)
+
+
+def test_route_of_more_tokens_than_a_launch_takes(c3gpu):
+    """2^26 tokens and some: each repeats one of 999 tokens, and gets that token's choice and gradient."""
+    import torch
+
+    rng = np.random.default_rng(6)
+    T, E, k, n = (1 << 26) + 77, 4, 2, 999
+    x = logits(rng, n, E, 0, 0.1)
+    dw = rng.normal(0, 1, (n, k)).astype(np.float32)
+    idx, w = run(c3gpu, x, 0, k)
+    few = gradient(c3gpu, x, 0, idx, dw, "softmax", True, 1.0)
+    want_i, want_w = ref.route(x, k)
+    np.testing.assert_array_equal(idx, want_i)
+    weights_close(x, idx, w, want_w)
+
+    again = lambda v: dev(v).repeat(T // n + 1, 1)[:T]  # noqa: E731
+    all_x, all_dw = again(x).bfloat16(), again(dw)
+    all_idx = torch.full((T + 1, k), -9, dtype=torch.int32, device="cuda:0")
+    all_w = torch.full((T + 1, k), -9.0, device="cuda:0")
+    d = torch.full((T + 1, E), -9.0, dtype=torch.bfloat16, device="cuda:0")
+    o = c3gpu.route_opts(top_k=k)
+    c3gpu.c3_route(all_x, 0, T, E, E, o, None, all_idx, all_w)
+    c3gpu.c3_route_backward(all_x, 0, T, E, E, o, all_idx, all_dw, d, E)
+    torch.cuda.synchronize()
+    assert (all_idx[T] == -9).all().item() and (all_w[T] == -9).all().item() and (d[T] == -9).all().item()
+    assert torch.equal(all_idx[:T], again(idx))
+    # another arrangement of the lanes adds in another order: both within the bound of the few
+    assert ((all_w[:T] - again(w)).abs() <= (40 + k) * 2.0 ** -23).all().item()
+    limit = again((2.0 ** -7 * np.abs(few) + 140 * 2.0 ** -23 * np.abs(dw).sum(1, keepdims=True)).astype(np.float32))
+    assert ((d[:T].float() - again(few.astype(np.float32))).abs() <= limit).all().item()
+    del all_x, all_dw, all_idx, all_w, d, limit
+    torch.cuda.empty_cache()
