@@ -323,53 +323,65 @@ __global__ __launch_bounds__(kThreads) void dequantize_rows(const void* __restri
 
 namespace c3 {
 
-// Workgroups of one launch: the runtime takes below 2^32 threads.
-static c3_status check_groups(const char* who, int64_t groups, int threads) {
-    if (groups >= (int64_t(1) << 32) / threads)
-        return fail(C3_E_INVALID, "%s: too large for one launch", who);
+// Rows [r, r + n) at a time, up to `most` of them: one launch takes below 2^32 threads.
+template <typename Launch>
+static c3_status in_parts(int64_t rows, int64_t most, Launch launch) {
+    for (int64_t r = 0; r < rows; r += most) {
+        launch(r, std::min(most, rows - r));
+        C3_HIP_TRY(hipGetLastError());
+    }
     return C3_OK;
+}
+// Workgroups of a launch, and rows of `per_row` pieces that they take (per_row < 2^29).
+constexpr int64_t kMostGroups = (int64_t(1) << 32) / kThreads - 1;
+static int64_t most_rows(uint32_t per_row) { return kMostGroups * kThreads * kPieces / per_row; }
+static dim3 groups_of(int64_t rows, uint32_t per_row) {
+    return dim3((unsigned)((rows * per_row + kThreads * kPieces - 1) / (kThreads * kPieces)));
 }
 
 c3_status mx4_quantize_enqueue(const Mx4Quant& q, hipStream_t stream) {
     const int64_t padded = mx4_padded(q.cols);
     const bool bf16 = q.dtype == C3_BF16;
+    const int size = bf16 ? 2 : 4;
     const char* x = static_cast<const char*>(q.x);
     if (q.transpose) {
-        const int narrow = bf16 ? 128 : 64, size = bf16 ? 2 : 4;
-        auto groups_of = [&](int tile) { return (q.rows + tile - 1) / tile * (padded / 256); };
+        const int narrow = bf16 ? 128 : 64;
+        const int64_t units = padded / 256;
         const bool wide = (((uintptr_t)x | (uint64_t)(q.ld * size)) & 7) == 0 &&
-                          groups_of(2 * narrow) >= 2 * std::max(c3::ctx().info.n_cu, 1);
+                          (q.rows + 2 * narrow - 1) / (2 * narrow) * units >= 2 * std::max(c3::ctx().info.n_cu, 1);
         const int tile = wide ? 2 * narrow : narrow;
-        const int64_t groups = groups_of(tile);
-        C3_TRY(check_groups("c3_mx4_quantize", groups, 512));
         auto kernel = bf16 ? (wide ? quantize_transposed<true, 2> : quantize_transposed<true, 1>)
                            : (wide ? quantize_transposed<false, 2> : quantize_transposed<false, 1>);
-        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(512), 0, stream, x, q.cols, q.rows,
-                           q.ld, (int)q.up, q.codes, q.scales, padded, (uint32_t)((q.rows + tile - 1) / tile));
-    } else {
-        const uint32_t per_row = (uint32_t)(padded / 8);
-        const int64_t groups = (q.rows * per_row + kThreads * kPieces - 1) / (kThreads * kPieces);
-        C3_TRY(check_groups("c3_mx4_quantize", groups, kThreads));
-        auto kernel = bf16 ? quantize_rows<true> : quantize_rows<false>;
-        hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream, x, q.rows, q.cols,
-                           q.ld, (int)q.up, reinterpret_cast<uint32_t*>(q.codes), q.scales, per_row,
-                           magic_of(per_row));
+        return in_parts(q.rows, (int64_t(1) << 22) * tile, [&](int64_t r, int64_t n) {
+            const int64_t tiles = (n + tile - 1) / tile, most = kMostGroups / 2 / tiles;  // of 512 threads
+            for (int64_t u = 0; u < units; u += most)
+                hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * std::min(most, units - u))), dim3(512), 0, stream,
+                                   x + (u * 256 * q.ld + r) * size, q.cols - u * 256, n, q.ld, (int)q.up,
+                                   q.codes + r * (padded / 2) + u * 128, q.scales + r * (padded / 32) + u * 8,
+                                   padded, (uint32_t)tiles);
+        });
     }
-    C3_HIP_TRY(hipGetLastError());
-    return C3_OK;
+    const uint32_t per_row = (uint32_t)(padded / 8);
+    auto kernel = bf16 ? quantize_rows<true> : quantize_rows<false>;
+    return in_parts(q.rows, most_rows(per_row), [&](int64_t r, int64_t n) {
+        hipLaunchKernelGGL(kernel, groups_of(n, per_row), dim3(kThreads), 0, stream, x + r * q.ld * size, n, q.cols,
+                           q.ld, (int)q.up, reinterpret_cast<uint32_t*>(q.codes) + r * per_row,
+                           q.scales + r * (padded / 32), per_row, magic_of(per_row));
+    });
 }
 
 c3_status mx4_dequantize_enqueue(const Mx4Quant& q, hipStream_t stream) {
-    const int values = q.dtype == C3_BF16 ? 8 : 4;  // of a lane's piece
+    const int64_t padded = mx4_padded(q.cols);
+    const bool bf16 = q.dtype == C3_BF16;
+    const int values = bf16 ? 8 : 4, size = bf16 ? 2 : 4;  // of a lane's piece, bytes of a value
     const uint32_t per_row = (uint32_t)((q.cols + values - 1) / values);
-    const int64_t groups = (q.rows * per_row + kThreads * kPieces - 1) / (kThreads * kPieces);
-    C3_TRY(check_groups("c3_mx4_dequantize", groups, kThreads));
-    auto kernel = q.dtype == C3_BF16 ? dequantize_rows<true> : dequantize_rows<false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(kThreads), 0, stream,
-                       static_cast<const void*>(q.codes), q.scales, q.rows, q.cols, q.ld,
-                       static_cast<char*>(q.y), mx4_padded(q.cols), per_row, magic_of(per_row));
-    C3_HIP_TRY(hipGetLastError());
-    return C3_OK;
+    auto kernel = bf16 ? dequantize_rows<true> : dequantize_rows<false>;
+    return in_parts(q.rows, most_rows(per_row), [&](int64_t r, int64_t n) {
+        hipLaunchKernelGGL(kernel, groups_of(n, per_row), dim3(kThreads), 0, stream,
+                           static_cast<const void*>(q.codes + r * (padded / 2)), q.scales + r * (padded / 32), n,
+                           q.cols, q.ld, static_cast<char*>(q.y) + r * q.ld * size, padded, per_row,
+                           magic_of(per_row));
+    });
 }
 
 }  // namespace c3

@@ -424,3 +424,28 @@ def test_experts_wide(c3gpu):
     close(C[:, some].double().cpu().numpy(), want, bound, 0)
     del b, sb, C
     torch.cuda.empty_cache()
+
+
+def test_quantise_more_rows_than_a_launch_takes(c3gpu):
+    """2^28 rows and some of one value each, which repeat 257 others."""
+    import torch
+
+    rng = np.random.default_rng(8)
+    n, rows = 257, (1 << 28) + 19
+    x = wide(rng, (n, 1))
+    want = ref.quantize(x)
+    t = typed(x, 0).repeat(rows // n + 1, 1)[:rows].contiguous()
+    nc, ns = c3gpu.c3_mx4_bytes(rows, 1)
+    codes = torch.full((nc + 64,), 0x5A, dtype=torch.uint8, device="cuda:0")
+    scales = torch.full((ns + 64,), 0x5A, dtype=torch.uint8, device="cuda:0")
+    c3gpu.c3_mx4_quantize(t, 0, rows, 1, 1, False, 0, codes, scales)
+    torch.cuda.synchronize()
+    assert (codes[nc:] == 0x5A).all().item() and (scales[ns:] == 0x5A).all().item()
+    step = n * 4096
+    for got, one in ((codes[:nc].view(rows, -1), want[0]), (scales[:ns].view(rows, -1), want[1])):
+        all_of = dev(one).repeat(4096, 1)
+        for r in range(0, rows, step):
+            part = got[r:r + step]
+            assert torch.equal(part, all_of[:len(part)]), r
+    del t, codes, scales, got, part
+    torch.cuda.empty_cache()
