@@ -253,7 +253,7 @@ c3_status c3_route_plan(const int32_t* idx, int64_t n_tokens, int top_k, int n_e
         if (top_k < 1 || top_k > C3_MAX_TOP_K)
             return fail(C3_E_INVALID, "c3_route_plan: top_k must be in [1, %d], got %d",
                         C3_MAX_TOP_K, top_k);
-        if (n_tokens < 0 || n_tokens >= (int64_t(1) << 31) / top_k)
+        if (n_tokens < 0 || n_tokens > ((int64_t(1) << 31) - 1) / top_k)
             return fail(C3_E_INVALID, "c3_route_plan: n_tokens * top_k must be in [0, 2^31)");
         const size_t slots = (size_t)n_tokens * top_k;
         C3_TRY(check_arrays("c3_route_plan",

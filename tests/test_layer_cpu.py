@@ -166,3 +166,12 @@ def test_definition_gradient_against_differences(kind, renorm):
             f = [(dw[t, :len(at)] * ref.weights_of(ref.clean(y), at, kind, renorm, 1.5)).sum() for y in (lo, hi)]
             # central difference: truncation below h^2 * 10, rounding below 1e-15 / h
             assert abs((f[1] - f[0]) / (2 * h) - d[t, e]) < 1e-9 + 1e-15 / h
+
+
+@pytest.mark.parametrize("top_k", [1, 2, 3, 5, 7, 64])
+def test_plan_takes_every_number_of_slots_below_its_limit(top_k):
+    """n_tokens * top_k < 2^31, whether top_k divides 2^31 or not."""
+    at = [n << 40 for n in (1, 2, 3)]
+    most = ((1 << 31) - 1) // top_k
+    assert c3.call("c3_route_plan", at[0], most, top_k, 8, at[1], at[2], None) == c3.C3_E_NOT_INIT
+    refused(c3.C3_E_INVALID, "n_tokens", "c3_route_plan", at[0], most + 1, top_k, 8, at[1], at[2], None)
