@@ -89,12 +89,14 @@ struct Sum {
     __device__ V operator()(V a, V b) const { return a + b; }
 };
 
-// e^x for x <= 0: x = n ln 2 + r in two parts of ln 2, then the Taylor series to r^13, |r| <= 0.35.
+// e^x for x <= 0: x = n ln 2 + r with ln 2 in two parts (Cody and Waite's reduction), its first 32
+// bits, 2^32 ln 2 cut to a whole number, whose product with n is exact, and the rest of it rounded;
+// then the Taylor series to r^13, |r| <= 0.35.
 __device__ __forceinline__ double exp64(double x) {
     x = __builtin_fmax(x, -800.0);  // 0 from -746 on
     const double n = __builtin_rint(x * 1.4426950408889634);
-    double r = __builtin_fma(-n, 6.93147180369123816490e-01, x);  // ln 2 rounded to 32 bits
-    r = __builtin_fma(-n, 1.90821492927058770002e-10, r);         // the rest of it
+    double r = __builtin_fma(-n, 0xb17217f7p-32, x);
+    r = __builtin_fma(-n, 0x1.a39ef35793c76p-33, r);
     double p = 1.0 / 6227020800.0;
     constexpr double f[13] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
                               1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
