@@ -121,7 +121,9 @@ __device__ __forceinline__ float sigmoid32(float l) {
 
 // A key orders by value, then by the lower index: the value's lowest bits (`low`, as many as an
 // index needs, at most 10 of 52) make way for the index, counted down where the value is not
-// negative. A logit leaves 29 bits free, so nothing of it is lost; s + bias keeps a relative 2^-42.
+// negative. A logit leaves 29 bits free, so nothing of it is lost; s + bias keeps a relative 2^-42
+// of itself, besides the rounding of s, below 2^-43 of s (the difference of two logits up to 800
+// apart rounds by 2^-44, the steps after it by a few 2^-53).
 __device__ __forceinline__ double key_of(double v, int i, uint32_t low) {
     v = __builtin_fmin(v, 1.7976931348623157e308) + 0.0;  // -0 as 0
     const uint64_t u = __builtin_bit_cast(uint64_t, v) & ~(uint64_t)low;

@@ -412,8 +412,9 @@ typedef struct {
  * With n_groups > 1 only experts of the token's top_groups best groups can be chosen: a group's
  * worth is its best expert's value (group_top = 1) or the sum of s + bias over its two best
  * (group_top = 2; one if it has one in reach).
- * Choices: logits are compared exactly; s + bias (and the sums of two) in 64-bit floating point,
- * in which values closer than a relative 2^-42 may go either way; equal s + bias never do.
+ * Choices: logits are compared exactly; s + bias (and the sums of two) in 64-bit floating point, in
+ * which values v closer than 2^-42 * (|v| + s) may go either way, s their scores (so where a bias
+ * nearly cancels s, its rounding decides); equal logits with equal biases never do.
  * weights: the chosen s, over their sum if renormalize (correct also where every s underflows),
  * times scale. Where fewer than top_k experts are in reach the rest have idx -1 and weight 0.
  * n_tokens = 0 is a no-op. 1 <= n_experts <= C3_MAX_EXPERTS, ld >= n_experts. */

@@ -453,3 +453,33 @@ def test_route_of_more_tokens_than_a_launch_takes(c3gpu):
     assert ((d[:T].float() - again(few.astype(np.float32))).abs() <= limit).all().item()
     del all_x, all_dw, all_idx, all_w, d, limit
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_where_the_bias_cancels_the_score(c3gpu, kind):
+    """Biases that are the scores' negatives rounded to fp32: what is left is a rounding of the
+    score, and a choice may only be out of order by the stated 2^-42 of |s + bias| and s."""
+    rng = np.random.default_rng(13)
+    T, E, k = 300, 64, 12
+    base = rng.normal(0, 1.5, E).astype(np.float32)
+    x = np.tile(base, (T, 1))
+    if kind == "sigmoid":
+        x = (x * (1 + rng.integers(-2, 3, (T, E)) * 2.0 ** -23)).astype(np.float32)
+    else:
+        x[1::2, 3] += (rng.integers(-2, 3, T // 2) * 2.0 ** -23).astype(np.float32)
+    wide = x.astype(np.longdouble)
+    if kind == "sigmoid":
+        s = 1 / (1 + np.exp(-wide))
+    else:
+        s = np.exp(wide - wide.max(1, keepdims=True))
+        s /= s.sum(1, keepdims=True)
+    bias = (-s[0]).astype(np.float32)
+    idx, _ = run(c3gpu, x, 1, k, kind, bias=bias)
+    v = s + bias.astype(np.longdouble)
+    slack = 2.0 ** -42 * (np.abs(v) + s)
+    for t in range(T):
+        chosen = idx[t]
+        assert len(set(chosen)) == k and (chosen >= 0).all()
+        rest = np.setdiff1d(np.arange(E), chosen)
+        for a, b in [*zip(chosen[:-1], chosen[1:]), *((chosen[-1], e) for e in rest)]:
+            assert v[t, a] >= v[t, b] - max(slack[t, a], slack[t, b]), (t, a, b)
