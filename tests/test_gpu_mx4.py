@@ -449,3 +449,23 @@ def test_quantise_more_rows_than_a_launch_takes(c3gpu):
             assert torch.equal(part, all_of[:len(part)]), r
     del t, codes, scales, got, part
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T,E,k,N,K,skew,absent", [
+    (3000, 64, 6, 520, 300, 0.5, 0.05), (1500, 70, 6, 140, 513, 1.5, 0.0), (1500, 70, 6, 700, 513, 0.5, 0.0),
+    (4000, 256, 8, 200, 300, 0.5, 0.1), (6000, 600, 16, 65, 300, 1.0, 0.02), (1500, 130, 8, 500, 300, 0.5, 0.02)])
+def test_experts_many_in_tiles(c3gpu, T, E, k, N, K, skew, absent, dtype):
+    """64 experts and more, with rows enough for the tile kernels."""
+    test_experts(c3gpu, T, E, k, N, K, skew, absent, False, True, dtype)
+
+
+@pytest.mark.parametrize("M,N,K", [(32, 1100, 16384), (20, 1000, 8200), (17, 520, 30000)])
+def test_product_few_rows_long_k(c3gpu, M, N, K):
+    """Up to sixteen waves a workgroup, which split K among them."""
+    test_product(c3gpu, M, N, K, 0)
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(40, 4, 2, 600, 9000), (100, 8, 2, 260, 8500), (6, 3, 2, 500, 20000)])
+def test_experts_few_rows_long_k(c3gpu, T, E, k, N, K):
+    test_experts(c3gpu, T, E, k, N, K, 0.3, 0.05, True, True, 1)
