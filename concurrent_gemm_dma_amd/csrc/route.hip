@@ -605,14 +605,19 @@ void choose(const c3::RouteArgs& a, Choice& c, hipStream_t stream) {
         return (c.size + (1 << log) - 1) >> log;
     };
     // Four tokens a wave do the reductions of four at once, at several times the length of a wave:
-    // for batches that fill the device. 128 experts, 32768 tokens: 11 us against 29 with one token
-    // a wave, 2049 tokens 5.4 against 5.1; 256 experts in 8 groups, 32768 tokens: 47 against 51,
-    // 4096 tokens 9.3 against 9.4, 2049 tokens 9.4 against 7.7.
+    // for batches that fill the device, the larger the more a wave holds and computes for each token.
+    // Times of four tokens a wave against one, in us, just above the border (or at it) and at 32768:
+    // up to 8 values a lane 2049: 4.5 / 4.5 (128 experts), 10.7 / 27.0;
+    // up to 16, in groups 2304: 6.4 / 6.7 (256 experts, 8 groups by their two best), 26.7 / 43.1;
+    // without groups 4096: 5.8 / 5.9, 14.4 / 28.0; with a bias 7168: 10.5 / 10.5, 28.8 / 38.5;
+    // with a bias and groups, of which a SIMD holds three such waves (133 registers) and ten of one
+    // token (46), 20000: 30.0 / 30.0, 24576: 34.6 / 35.2, 44.9 / 46.3 (9.0 / 8.5 at 4096, 14.3 / 9.6 at 5000).
     if (a.T > 2048 && c.k <= 16) {
         const int n = values(16);
         if (n <= 4) return launch_choice<T, 16, 4>(a, c, stream);
         if (n <= 8) return launch_choice<T, 16, 8>(a, c, stream);
-        if (n <= 16 && a.T > 4096) return launch_choice<T, 16, 16>(a, c, stream);
+        const int64_t most = c.groups > 1 ? (a.bias ? 24576 : 2304) : (a.bias ? 7168 : 4096);
+        if (n <= 16 && a.T > most) return launch_choice<T, 16, 16>(a, c, stream);
     }
     const int n = values(64);
     if (n <= 1) return launch_choice<T, 64, 1>(a, c, stream);
@@ -632,11 +637,16 @@ void launch_gradient(const c3::RouteArgs& a, hipStream_t stream) {
 
 template <typename T>
 void gradient(const c3::RouteArgs& a, hipStream_t stream) {
-    // as for the choice: 32768 tokens of 256 experts 11 us against 17 with one token a wave (softmax
-    // over all 18 against 22), 8192 5.1 against 6.2, 4096 5.0 against 4.9 (6.8 against 5.2)
-    if (a.T > 4096 && a.o.top_k <= 16 && a.E <= 256) {
-        if (a.E <= 64) return launch_gradient<T, 16, 4>(a, stream);
-        return a.E <= 128 ? launch_gradient<T, 16, 8>(a, stream) : launch_gradient<T, 16, 16>(a, stream);
+    // As for the choice; softmax over all experts costs four tokens a wave more. Times of four tokens a
+    // wave against one, in us, 8 choices: over the chosen, 64 experts 3073: 3.0 / 3.0, 128 experts 5120:
+    // 3.8 / 3.8, 256 experts 6144: 4.8 / 5.0 (4.8 / 4.3 where sigmoid scores are not renormalised);
+    // over all, 64 experts 4608: 3.6 / 3.8 (3.6 / 3.5 at 4096), 128 experts 6144: 4.8 / 4.7 and 7168:
+    // 4.9 / 5.0, 256 experts 10240: 8.5 / 8.7 (bf16 8.8 / 8.4).
+    const bool over_all = a.o.score == C3_SCORE_SOFTMAX && !a.o.renormalize;
+    if (a.o.top_k <= 16) {
+        if (a.E <= 64 && a.T > (over_all ? 4096 : 3072)) return launch_gradient<T, 16, 4>(a, stream);
+        if (a.E > 64 && a.E <= 128 && a.T > (over_all ? 6656 : 5120)) return launch_gradient<T, 16, 8>(a, stream);
+        if (a.E > 128 && a.E <= 256 && a.T > (over_all ? 10240 : 6144)) return launch_gradient<T, 16, 16>(a, stream);
     }
     if (a.E <= 64) return launch_gradient<T, 64, 1>(a, stream);
     if (a.E <= 128) return launch_gradient<T, 64, 2>(a, stream);

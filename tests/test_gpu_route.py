@@ -483,3 +483,49 @@ def test_route_where_the_bias_cancels_the_score(c3gpu, kind):
         rest = np.setdiff1d(np.arange(E), chosen)
         for a, b in [*zip(chosen[:-1], chosen[1:]), *((chosen[-1], e) for e in rest)]:
             assert v[t, a] >= v[t, b] - max(slack[t, a], slack[t, b]), (t, a, b)
+
+
+def repeated(x, T):
+    return np.resize(x, (T, x.shape[1]))
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("case", [
+    dict(T=24580, E=256, k=8, kind="sigmoid", groups=8, top_groups=4, group_top=2, bias=True),
+    dict(T=24579, E=252, k=5, groups=4, top_groups=2, bias=True), dict(T=7171, E=250, k=9, bias=True),
+    dict(T=7170, E=201, k=16, kind="sigmoid", bias=True, renorm=False), dict(T=4097, E=255, k=7),
+    dict(T=2305, E=256, k=8, kind="sigmoid", groups=8, top_groups=4, group_top=2), dict(T=2306, E=160, k=6, groups=8,
+                                                                                       top_groups=3)],
+    ids=lambda c: "-".join(str(v) for v in c.values()))
+def test_route_four_tokens_a_wave(c3gpu, case, dtype):
+    """Past the batch from which 129 to 256 experts take four tokens a wave, of each form."""
+    c = dict(case)
+    T, E, k = c.pop("T"), c.pop("E"), c.pop("k")
+    rng = np.random.default_rng(T + E)
+    few = logits(rng, 301, E, dtype, 0.1)
+    c["bias"] = (0.1 * rng.normal(0, 1, E)).astype(np.float32) if c.get("bias") else None
+    idx, w = run(c3gpu, repeated(few, T), dtype, k, ld=E + 1, **c)
+    want_i, want_w = ref.route(few, k, **c)
+    np.testing.assert_array_equal(idx, repeated(want_i, T))
+    weights_close(few, want_i, w[:301], want_w)
+    weights_close(repeated(few, T)[-301:], want_i, w[-301:], repeated(want_w, T)[-301:])
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T,E,k,kind,renorm", [
+    (3075, 33, 6, "sigmoid", False), (4099, 64, 16, "softmax", False), (5122, 127, 8, "softmax", True),
+    (6658, 100, 8, "softmax", False), (6147, 256, 8, "sigmoid", True), (10243, 255, 16, "softmax", False)])
+def test_route_backward_four_tokens_a_wave(c3gpu, T, E, k, kind, renorm, dtype):
+    rng = np.random.default_rng(T + E)
+    few = logits(rng, 301, E, dtype, 0.1)
+    idx, _ = ref.route(few, k, kind)
+    idx[3], idx[4, 1], idx[5, 0] = -1, E, -7
+    idx[6, 1] = idx[6, 0]
+    dw = rng.normal(0, 1, (301, k)).astype(np.float32)
+    got = gradient(c3gpu, repeated(few, T), dtype, repeated(idx, T), repeated(dw, T), kind, renorm, 1.5, ld=E + 3)
+    want, size = (repeated(v, T) for v in ref.route_gradient(few, idx, dw, kind, renorm, 1.5))
+    half = 2.0 ** -8 if dtype == 0 else 2.0 ** -24
+    # as in test_route_backward
+    limit = (40 + 24 + k + E / 8) * 2.0 ** -24 * size + half * np.abs(want) + 2.0 ** -126
+    bad = ~(np.abs(got - want) <= limit)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
