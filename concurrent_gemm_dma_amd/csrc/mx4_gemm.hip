@@ -274,8 +274,8 @@ __global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void mx4_gemm_rows(const
 // j of its half h is byte 2 * h + j of the lane's register, which the instruction selects at no
 // cost.
 //
-// 8192x53248x16384 2.97 ms, 4.8 PFLOP/s; 8192x8192x8192 0.26 ms with the matrix pipe busy 60% of
-// the cycles at 1.72 GHz. Matrix instructions alone, operands in registers and random, run at 6.4
+// 8192x53248x16384 2.94-3.06 ms on three cards, 4.7-4.8 PFLOP/s; 8192x8192x8192 0.26 ms, the matrix pipe busy 60% of
+// the cycles at 1.66-1.72 GHz. Matrix instructions alone, operands in registers and random, run at 6.4
 // PFLOP/s here (power holds the clock near 1.57 GHz; 9.7 on zeros). A tile's start and end cost a
 // CU 10-14 us (stores 5, their way through LDS 3-4), which short K shows: 16384 slots of 8 experts x
 // 14336x4096 0.61 ms, 3.1 PFLOP/s.

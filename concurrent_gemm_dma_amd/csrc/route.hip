@@ -173,7 +173,7 @@ struct Choice {
 // the two best of a group); weights in 32.
 //
 // Bound by instructions: 32768 tokens of 128 experts, bf16, 8 each 11-12 us, of 256 experts in 8
-// groups with a bias 47 us (a 64-bit exponential for every expert); one token of those 4.2 us,
+// groups with a bias 45 us (a 64-bit exponential for every expert); one token of those 4.2 us,
 // memory latencies and the rounds in turn.
 template <typename T, int W, int NV, bool BIAS>
 __global__ __launch_bounds__(256) void route_tokens(const T* __restrict__ logits, const Choice c,
@@ -330,9 +330,9 @@ __global__ __launch_bounds__(256) void route_tokens(const T* __restrict__ logits
 // W lanes a token (64, or 16 with four tokens a wave); lane j holds the j-th choice. Value i of a
 // lane is expert R * (W * (i / R) + lane) + i % R, where R values make a word of dlogits.
 // sigmoid: dl = g s (1 - s), renormalised (1 - s) w (g - sum g w); softmax: p (g - sum g p) over
-// all in reach, renormalised the same over the chosen alone. 8192 tokens of 256 experts, bf16, 5.1 us,
+// all in reach, renormalised the same over the chosen alone. 8192 tokens of 256 experts, bf16, 4.8 us,
 // of which a launch is 2 and the bytes at a copy's rate 1.4: the rest is the chain of a wave's loads
-// (index, logit) and reductions. 32768 tokens 11 us.
+// (index, logit) and reductions. 32768 tokens 11 us, softmax over all 18.
 template <typename T, int W, int NV>
 __global__ __launch_bounds__(256) void route_gradient(const T* __restrict__ logits,
                                                       int64_t n_tokens, int E, int64_t ld,
@@ -610,7 +610,7 @@ void choose(const c3::RouteArgs& a, Choice& c, hipStream_t stream) {
     // up to 8 values a lane 2049: 4.5 / 4.5 (128 experts), 10.7 / 27.0;
     // up to 16, in groups 2304: 6.4 / 6.7 (256 experts, 8 groups by their two best), 26.7 / 43.1;
     // without groups 4096: 5.8 / 5.9, 14.4 / 28.0; with a bias 7168: 10.5 / 10.5, 28.8 / 38.5;
-    // with a bias and groups, of which a SIMD holds three such waves (133 registers) and ten of one
+    // with a bias and groups, of which a SIMD holds three such waves (133 registers) and eight of one
     // token (46), 20000: 30.0 / 30.0, 24576: 34.6 / 35.2, 44.9 / 46.3 (9.0 / 8.5 at 4096, 14.3 / 9.6 at 5000).
     if (a.T > 2048 && c.k <= 16) {
         const int n = values(16);

@@ -375,6 +375,8 @@ c3_status c3_flush_llc(size_t bytes, void* stream);
  *
  * Every call here is stream-ordered, asynchronous and deterministic (no atomics in any result,
  * fixed summation order). Buffers a call writes must not overlap those it reads (C3_E_OVERLAP).
+ * Numbers of tokens and row strides are below 2^31, top_k up to C3_MAX_TOP_K. Products of operands
+ * may flush terms and sums below fp32's smallest normal, 2^-126, to zero.
  * ------------------------------------------------------------------------------------------- */
 
 typedef enum { C3_BF16 = 0, C3_F32 = 1 } c3_dtype;
