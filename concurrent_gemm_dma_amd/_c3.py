@@ -40,7 +40,7 @@ C3_MAX_MASK_WORDS = 8
 C3_MAX_WORLD = 64
 C3_MAX_CURVE = 16
 C3_NOALLOC_SCRATCH_BYTES = 16 << 20  # c3_gemm_noalloc: fixed split-K partials per device
-C3_ABI_VERSION = 6
+C3_ABI_VERSION = 7
 C3_BF16 = 0
 C3_F32 = 1
 C3_SCORE_SOFTMAX = 0
@@ -48,6 +48,8 @@ C3_SCORE_SIGMOID = 1
 C3_MX4_FLOOR = 0
 C3_MX4_UP = 1
 C3_MX4_PAD = 256
+C3_I8_PAD = 128
+C3_I8_MAX_K = 131071
 C3_MAX_EXPERTS = 1024
 C3_MAX_TOP_K = 64
 C3_PLAN_WORKSPACE_BYTES = 2 << 20
@@ -59,7 +61,10 @@ EXPORTS = ("c3_init", "c3_finalize", "c3_last_error", "c3_device_info", "c3_stre
            "c3_gemm_noalloc", "c3_probe_mfma_rate",
            "c3_gather", "c3_all2all_block", "c3_reduce_scatter", "c3_allreduce_local",
            "c3_route", "c3_route_backward", "c3_route_plan", "c3_mx4_bytes", "c3_mx4_quantize",
-           "c3_mx4_dequantize", "c3_mx4_gemm", "c3_mx4_gemm_experts", "c3_flush_llc", "c3_run_concurrent", "c3_derive_metrics", "c3_roofline_time",
+           "c3_mx4_dequantize", "c3_mx4_gemm", "c3_mx4_gemm_experts", "c3_dispatch",
+           "c3_combine", "c3_combine_backward", "c3_i8_bytes", "c3_i8_quantize", "c3_i8_dispatch",
+           "c3_i8_dequantize", "c3_i8_gemm", "c3_i8_gemm_experts",
+           "c3_flush_llc", "c3_run_concurrent", "c3_derive_metrics", "c3_roofline_time",
            "c3_predict_partition", "c3_hybrid_share")
 
 
@@ -210,6 +215,15 @@ def load(path: Optional[str] = None):
     L.c3_mx4_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
     L.c3_mx4_gemm_experts.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i64,
                                       i64, i64, vp]
+    L.c3_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i32, vp, i64, vp, vp]
+    L.c3_combine.argtypes = [vp, i32, i64, i32, i64, i64, vp, vp, vp, i64, vp]
+    L.c3_combine_backward.argtypes = [vp, i32, i64, i32, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp]
+    L.c3_i8_bytes.argtypes = L.c3_mx4_bytes.argtypes
+    L.c3_i8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.c3_i8_dispatch.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i32, vp, vp, vp, vp]
+    L.c3_i8_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    L.c3_i8_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    L.c3_i8_gemm_experts.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i64, i64, i64, vp]
     L.c3_flush_llc.argtypes = [ctypes.c_size_t, vp]
     L.c3_run_concurrent.argtypes = [ctypes.POINTER(c3_gemm_args), ctypes.POINTER(c3_copy_args),
                                     ctypes.POINTER(c3_conc_opts), ctypes.POINTER(c3_timing)]
@@ -416,6 +430,63 @@ def c3_mx4_gemm_experts(A, sA, a_rows: int, B, sB, order, offsets, weights, C, d
     check(load().c3_mx4_gemm_experts(_ptr(A), _ptr(sA), a_rows, _ptr(B), _ptr(sB), _ptr(order),
                                      _ptr(offsets), _ptr(weights), _ptr(C), dtype, n_tokens, top_k,
                                      n_experts, N, K, ldc, _stream(stream)))
+
+
+def c3_dispatch(x, dtype: int, n_tokens: int, cols: int, ld: int, order, offsets, top_k: int,
+                n_experts: int, y, ld_y: int, pos, stream=None) -> None:
+    check(load().c3_dispatch(_ptr(x), dtype, n_tokens, cols, ld, _ptr(order), _ptr(offsets), top_k,
+                             n_experts, _ptr(y), ld_y, _ptr(pos), _stream(stream)))
+
+
+def c3_combine(y, dtype: int, n_tokens: int, top_k: int, cols: int, ld_y: int, pos, weights, out,
+               ld_out: int, stream=None) -> None:
+    check(load().c3_combine(_ptr(y), dtype, n_tokens, top_k, cols, ld_y, _ptr(pos), _ptr(weights),
+                            _ptr(out), ld_out, _stream(stream)))
+
+
+def c3_combine_backward(dout, dtype: int, n_tokens: int, top_k: int, cols: int, ld_d: int, y,
+                        ld_y: int, pos, weights, dy, ld_dy: int, dweights, stream=None) -> None:
+    check(load().c3_combine_backward(_ptr(dout), dtype, n_tokens, top_k, cols, ld_d, _ptr(y), ld_y,
+                                     _ptr(pos), _ptr(weights), _ptr(dy), ld_dy, _ptr(dweights),
+                                     _stream(stream)))
+
+
+def c3_i8_bytes(rows: int, cols: int) -> tuple:
+    """(bytes of codes, bytes of scales) of an int8 operand of rows x cols."""
+    codes, scales = ctypes.c_size_t(), ctypes.c_size_t()
+    check(load().c3_i8_bytes(rows, cols, ctypes.byref(codes), ctypes.byref(scales)))
+    return codes.value, scales.value
+
+
+def c3_i8_quantize(x, dtype: int, rows: int, cols: int, ld: int, codes, scales,
+                   stream=None) -> None:
+    check(load().c3_i8_quantize(_ptr(x), dtype, rows, cols, ld, _ptr(codes), _ptr(scales),
+                                _stream(stream)))
+
+
+def c3_i8_dispatch(x, dtype: int, n_tokens: int, cols: int, ld: int, order, offsets, top_k: int,
+                   n_experts: int, codes, scales, pos, stream=None) -> None:
+    check(load().c3_i8_dispatch(_ptr(x), dtype, n_tokens, cols, ld, _ptr(order), _ptr(offsets),
+                                top_k, n_experts, _ptr(codes), _ptr(scales), _ptr(pos),
+                                _stream(stream)))
+
+
+def c3_i8_dequantize(codes, scales, rows: int, cols: int, y, dtype: int, ld: int,
+                     stream=None) -> None:
+    check(load().c3_i8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(y), dtype, ld,
+                                  _stream(stream)))
+
+
+def c3_i8_gemm(A, sA, B, sB, C, dtype: int, M: int, N: int, K: int, ldc: int,
+               stream=None) -> None:
+    check(load().c3_i8_gemm(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(C), dtype, M, N, K, ldc,
+                            _stream(stream)))
+
+
+def c3_i8_gemm_experts(A, sA, B, sB, offsets, C, dtype: int, n_rows: int, n_experts: int, N: int,
+                       K: int, ldc: int, stream=None) -> None:
+    check(load().c3_i8_gemm_experts(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(offsets), _ptr(C),
+                                    dtype, n_rows, n_experts, N, K, ldc, _stream(stream)))
 
 
 def _opts(o):

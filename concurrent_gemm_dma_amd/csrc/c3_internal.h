@@ -194,6 +194,48 @@ struct Mx4Gemm {
     int64_t a_rows = 0;
 };
 c3_status mx4_gemm_enqueue(const Mx4Gemm& g, hipStream_t stream);
+
+// ---- tokens sorted by expert (sort.hip) and int8 operands (i8.hip, i8_gemm.hip) ------------------
+struct SortArgs {
+    c3_dtype dtype = C3_BF16;
+    int64_t T = 0, cols = 0;
+    int top_k = 0, E = 0;
+    const void* x = nullptr;  // by token: dispatch's x, combine's out (written through out), dout
+    int64_t ld_x = 0;
+    const int32_t *order = nullptr, *offsets = nullptr;
+    int32_t* pos = nullptr;   // dispatch: written, otherwise read
+    const void* y = nullptr;  // by row: read by combine and its gradient
+    int64_t ld_y = 0;
+    void* out = nullptr;      // dispatch's y, combine's out, the gradient's dy
+    int64_t ld_out = 0;
+    const float* weights = nullptr;
+    float* dweights = nullptr;
+    float* scales = nullptr;  // int8 rows: out holds codes
+};
+c3_status dispatch_enqueue(const SortArgs& a, hipStream_t stream);
+c3_status combine_enqueue(const SortArgs& a, hipStream_t stream);
+c3_status combine_backward_enqueue(const SortArgs& a, hipStream_t stream);
+// pos[order[p]] = p below offsets[E], -1 past it.
+c3_status positions_enqueue(const SortArgs& a, hipStream_t stream);
+
+constexpr int64_t i8_padded(int64_t cols) { return (cols + C3_I8_PAD - 1) / C3_I8_PAD * C3_I8_PAD; }
+// Quantise every row of x (order == nullptr), or the rows sorted by expert.
+c3_status i8_quantize_enqueue(const SortArgs& a, hipStream_t stream);
+c3_status i8_dequantize_enqueue(const void* codes, const float* scales, int64_t rows, int64_t cols,
+                                void* y, c3_dtype dtype, int64_t ld, hipStream_t stream);
+
+struct I8Gemm {
+    const int8_t *A = nullptr, *B = nullptr;
+    const float *sA = nullptr, *sB = nullptr;
+    void* C = nullptr;
+    c3_dtype dtype = C3_BF16;
+    int M = 0, N = 0, K = 0;
+    int64_t ldc = 0;
+    const int32_t* offsets = nullptr;  // experts: the rows of each
+    int E = 1;
+};
+c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream);
+
 // A stream that the library is about to destroy: its workspace is free for another one.
 void layer_forget_stream(hipStream_t stream);
 void layer_release_workspaces();

@@ -1,5 +1,6 @@
-// layer.cpp -- the extern "C" entry points of expert layers (routing, MX FP4 operands and their
-// products) declared in include/c3.h: every argument is checked before any launch.
+// layer.cpp -- the extern "C" entry points of expert layers (routing, MX FP4 and int8 operands and
+// their products, rows sorted by expert) declared in include/c3.h: every argument is checked before
+// any launch.
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -160,6 +161,38 @@ c3_status check_operand(const char* who, int64_t rows, int64_t cols) {
 
 size_t codes_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (mx4_padded(cols) / 2); }
 size_t scales_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (mx4_padded(cols) / 32); }
+size_t i8_bytes(int64_t rows, int64_t cols) { return (size_t)rows * i8_padded(cols); }
+
+c3_status check_cols(const char* who, int64_t cols) {
+    if (cols < 1 || cols >= (int64_t(1) << 31))
+        return fail(C3_E_INVALID, "%s: cols must be in [1, 2^31), got %lld", who, (long long)cols);
+    return C3_OK;
+}
+
+c3_status check_slots(const char* who, int64_t n_tokens, int top_k) {
+    if (top_k < 1 || top_k > C3_MAX_TOP_K)
+        return fail(C3_E_INVALID, "%s: top_k must be in [1, %d], got %d", who, C3_MAX_TOP_K, top_k);
+    if (n_tokens < 0 || n_tokens > ((int64_t(1) << 31) - 1) / top_k)
+        return fail(C3_E_INVALID, "%s: n_tokens * top_k must be in [0, 2^31)", who);
+    return C3_OK;
+}
+
+c3_status check_experts(const char* who, int n_experts) {
+    if (n_experts < 1 || n_experts > C3_MAX_EXPERTS)
+        return fail(C3_E_INVALID, "%s: n_experts must be in [1, %d], got %d", who, C3_MAX_EXPERTS,
+                    n_experts);
+    return C3_OK;
+}
+
+c3_status check_i8_product(const char* who, int64_t N, int64_t K, int64_t ldc) {
+    if (N < 0 || N > kMaxGemmDim)
+        return fail(C3_E_INVALID, "%s: N must be in [0, %lld], got %lld", who,
+                    (long long)kMaxGemmDim, (long long)N);
+    if (K < 1 || K > C3_I8_MAX_K)
+        return fail(C3_E_INVALID, "%s: K must be in [1, %d], got %lld", who, C3_I8_MAX_K,
+                    (long long)K);
+    return check_ld(who, "ldc", N, ldc);
+}
 
 }  // namespace
 
@@ -426,6 +459,277 @@ c3_status c3_mx4_gemm_experts(const void* A, const void* sA, int64_t a_rows, con
         g.E = n_experts;
         g.a_rows = a_rows;
         return mx4_gemm_enqueue(g, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_t cols, int64_t ld,
+                      const int32_t* order, const int32_t* offsets, int top_k, int n_experts,
+                      void* y, int64_t ld_y, int32_t* pos, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_dispatch";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_slots(who, n_tokens, top_k));
+        C3_TRY(check_experts(who, n_experts));
+        C3_TRY(check_cols(who, cols));
+        C3_TRY(check_ld(who, "ld", cols, ld));
+        C3_TRY(check_ld(who, "ld_y", cols, ld_y));
+        if (n_tokens == 0) return require_init();
+        const size_t size = size_of(dtype);
+        const size_t slots = (size_t)n_tokens * top_k;
+        C3_TRY(check_arrays(
+            who, {{x, strided_bytes(n_tokens, cols, ld, size), size, "x", false},
+                  {order, slots * 4, 4, "order", false},
+                  {offsets, (size_t)(n_experts + 1) * 4, 4, "offsets", false},
+                  {y, strided_bytes((int64_t)slots, cols, ld_y, size), size, "y", true},
+                  {pos, slots * 4, 4, "pos", true}}));
+        SortArgs a;
+        a.dtype = dtype;
+        a.T = n_tokens;
+        a.cols = cols;
+        a.top_k = top_k;
+        a.E = n_experts;
+        a.x = x;
+        a.ld_x = ld;
+        a.order = order;
+        a.offsets = offsets;
+        a.pos = pos;
+        a.out = y;
+        a.ld_out = ld_y;
+        return dispatch_enqueue(a, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_combine(const void* y, c3_dtype dtype, int64_t n_tokens, int top_k, int64_t cols,
+                     int64_t ld_y, const int32_t* pos, const float* weights, void* out,
+                     int64_t ld_out, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_combine";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_slots(who, n_tokens, top_k));
+        C3_TRY(check_cols(who, cols));
+        C3_TRY(check_ld(who, "ld_y", cols, ld_y));
+        C3_TRY(check_ld(who, "ld_out", cols, ld_out));
+        if (n_tokens == 0) return require_init();
+        const size_t size = size_of(dtype);
+        const size_t slots = (size_t)n_tokens * top_k;
+        C3_TRY(check_arrays(
+            who, {{y, strided_bytes((int64_t)slots, cols, ld_y, size), size, "y", false},
+                  {pos, slots * 4, 4, "pos", false},
+                  {weights, weights ? slots * 4 : 0, 4, "weights", false},
+                  {out, strided_bytes(n_tokens, cols, ld_out, size), size, "out", true}}));
+        SortArgs a;
+        a.dtype = dtype;
+        a.T = n_tokens;
+        a.cols = cols;
+        a.top_k = top_k;
+        a.y = y;
+        a.ld_y = ld_y;
+        a.pos = const_cast<int32_t*>(pos);
+        a.weights = weights;
+        a.out = out;
+        a.ld_out = ld_out;
+        return combine_enqueue(a, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_combine_backward(const void* dout, c3_dtype dtype, int64_t n_tokens, int top_k,
+                              int64_t cols, int64_t ld_d, const void* y, int64_t ld_y,
+                              const int32_t* pos, const float* weights, void* dy, int64_t ld_dy,
+                              float* dweights, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_combine_backward";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_slots(who, n_tokens, top_k));
+        C3_TRY(check_cols(who, cols));
+        C3_TRY(check_ld(who, "ld_d", cols, ld_d));
+        if (dweights) C3_TRY(check_ld(who, "ld_y", cols, ld_y));
+        C3_TRY(check_ld(who, "ld_dy", cols, ld_dy));
+        if (n_tokens == 0) return require_init();
+        const size_t size = size_of(dtype);
+        const size_t slots = (size_t)n_tokens * top_k;
+        const size_t y_bytes = dweights ? strided_bytes((int64_t)slots, cols, ld_y, size) : 0;
+        C3_TRY(check_arrays(
+            who, {{dout, strided_bytes(n_tokens, cols, ld_d, size), size, "dout", false},
+                  {y, y_bytes, size, "y", false},
+                  {pos, slots * 4, 4, "pos", false},
+                  {weights, weights ? slots * 4 : 0, 4, "weights", false},
+                  {dy, strided_bytes((int64_t)slots, cols, ld_dy, size), size, "dy", true},
+                  {dweights, dweights ? slots * 4 : 0, 4, "dweights", true}}));
+        SortArgs a;
+        a.dtype = dtype;
+        a.T = n_tokens;
+        a.cols = cols;
+        a.top_k = top_k;
+        a.x = dout;
+        a.ld_x = ld_d;
+        a.y = y;
+        a.ld_y = ld_y;
+        a.pos = const_cast<int32_t*>(pos);
+        a.weights = weights;
+        a.out = dy;
+        a.ld_out = ld_dy;
+        a.dweights = dweights;
+        return combine_backward_enqueue(a, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_i8_bytes(int64_t rows, int64_t cols, size_t* codes, size_t* scales) {
+    C3_ENTRY({
+        C3_TRY(check_operand("c3_i8_bytes", rows, cols));
+        C3_TRY(check_cols("c3_i8_bytes", cols));
+        if (codes) *codes = i8_bytes(rows, cols);
+        if (scales) *scales = (size_t)rows * 4;
+        return C3_OK;
+    })
+}
+
+c3_status c3_i8_quantize(const void* x, c3_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                         void* codes, float* scales, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_i8_quantize";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_operand(who, rows, cols));
+        C3_TRY(check_cols(who, cols));
+        C3_TRY(check_ld(who, "ld", cols, ld));
+        if (rows == 0) return require_init();
+        const size_t size = size_of(dtype);
+        C3_TRY(check_arrays(who, {{x, strided_bytes(rows, cols, ld, size), size, "x", false},
+                                  {codes, i8_bytes(rows, cols), 16, "codes", true},
+                                  {scales, (size_t)rows * 4, 4, "scales", true}}));
+        SortArgs a;
+        a.dtype = dtype;
+        a.T = rows;
+        a.cols = cols;
+        a.top_k = 1;
+        a.x = x;
+        a.ld_x = ld;
+        a.out = codes;
+        a.scales = scales;
+        return i8_quantize_enqueue(a, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_i8_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_t cols, int64_t ld,
+                         const int32_t* order, const int32_t* offsets, int top_k, int n_experts,
+                         void* codes, float* scales, int32_t* pos, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_i8_dispatch";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_slots(who, n_tokens, top_k));
+        C3_TRY(check_experts(who, n_experts));
+        C3_TRY(check_cols(who, cols));
+        C3_TRY(check_ld(who, "ld", cols, ld));
+        if (n_tokens == 0) return require_init();
+        const size_t size = size_of(dtype);
+        const size_t slots = (size_t)n_tokens * top_k;
+        C3_TRY(check_arrays(
+            who, {{x, strided_bytes(n_tokens, cols, ld, size), size, "x", false},
+                  {order, slots * 4, 4, "order", false},
+                  {offsets, (size_t)(n_experts + 1) * 4, 4, "offsets", false},
+                  {codes, i8_bytes((int64_t)slots, cols), 16, "codes", true},
+                  {scales, slots * 4, 4, "scales", true},
+                  {pos, slots * 4, 4, "pos", true}}));
+        SortArgs a;
+        a.dtype = dtype;
+        a.T = n_tokens;
+        a.cols = cols;
+        a.top_k = top_k;
+        a.E = n_experts;
+        a.x = x;
+        a.ld_x = ld;
+        a.order = order;
+        a.offsets = offsets;
+        a.pos = pos;
+        a.out = codes;
+        a.scales = scales;
+        return i8_quantize_enqueue(a, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_i8_dequantize(const void* codes, const float* scales, int64_t rows, int64_t cols,
+                           void* y, c3_dtype dtype, int64_t ld, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_i8_dequantize";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_operand(who, rows, cols));
+        C3_TRY(check_cols(who, cols));
+        C3_TRY(check_ld(who, "ld", cols, ld));
+        if (rows == 0) return require_init();
+        const size_t size = size_of(dtype);
+        C3_TRY(check_arrays(who, {{codes, i8_bytes(rows, cols), 16, "codes", false},
+                                  {scales, (size_t)rows * 4, 4, "scales", false},
+                                  {y, strided_bytes(rows, cols, ld, size), size, "y", true}}));
+        return i8_dequantize_enqueue(codes, scales, rows, cols, y, dtype, ld,
+                                     static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_i8_gemm(const void* A, const float* sA, const void* B, const float* sB, void* C,
+                     c3_dtype dtype, int64_t M, int64_t N, int64_t K, int64_t ldc, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_i8_gemm";
+        C3_TRY(check_dtype(who, dtype));
+        if (M < 0 || M > kMaxGemmDim)
+            return fail(C3_E_INVALID, "%s: M must be in [0, %lld], got %lld", who,
+                        (long long)kMaxGemmDim, (long long)M);
+        C3_TRY(check_i8_product(who, N, K, ldc));
+        if (M == 0 || N == 0) return require_init();
+        const size_t size = size_of(dtype);
+        C3_TRY(check_arrays(who, {{A, i8_bytes(M, K), 16, "A", false},
+                                  {sA, (size_t)M * 4, 4, "sA", false},
+                                  {B, i8_bytes(N, K), 16, "B", false},
+                                  {sB, (size_t)N * 4, 4, "sB", false},
+                                  {C, strided_bytes(M, N, ldc, size), size, "C", true}}));
+        I8Gemm g;
+        g.A = static_cast<const int8_t*>(A);
+        g.B = static_cast<const int8_t*>(B);
+        g.sA = sA;
+        g.sB = sB;
+        g.C = C;
+        g.dtype = dtype;
+        g.M = (int)M;
+        g.N = (int)N;
+        g.K = (int)K;
+        g.ldc = ldc;
+        return i8_gemm_enqueue(g, static_cast<hipStream_t>(stream));
+    })
+}
+
+c3_status c3_i8_gemm_experts(const void* A, const float* sA, const void* B, const float* sB,
+                             const int32_t* offsets, void* C, c3_dtype dtype, int64_t n_rows,
+                             int n_experts, int64_t N, int64_t K, int64_t ldc, void* stream) {
+    C3_ENTRY({
+        const char* who = "c3_i8_gemm_experts";
+        C3_TRY(check_dtype(who, dtype));
+        C3_TRY(check_experts(who, n_experts));
+        if (n_rows < 0 || n_rows > kMaxSlots)
+            return fail(C3_E_INVALID, "%s: n_rows must be in [0, %lld], got %lld", who,
+                        (long long)kMaxSlots, (long long)n_rows);
+        C3_TRY(check_i8_product(who, N, K, ldc));
+        if (n_rows == 0 || N == 0) return require_init();
+        const size_t size = size_of(dtype);
+        const int64_t b_rows = (int64_t)n_experts * N;
+        C3_TRY(check_arrays(
+            who, {{A, i8_bytes(n_rows, K), 16, "A", false},
+                  {sA, (size_t)n_rows * 4, 4, "sA", false},
+                  {B, i8_bytes(b_rows, K), 16, "B", false},
+                  {sB, (size_t)b_rows * 4, 4, "sB", false},
+                  {offsets, (size_t)(n_experts + 1) * 4, 4, "offsets", false},
+                  {C, strided_bytes(n_rows, N, ldc, size), size, "C", true}}));
+        I8Gemm g;
+        g.A = static_cast<const int8_t*>(A);
+        g.B = static_cast<const int8_t*>(B);
+        g.sA = sA;
+        g.sB = sB;
+        g.C = C;
+        g.dtype = dtype;
+        g.M = (int)n_rows;
+        g.N = (int)N;
+        g.K = (int)K;
+        g.ldc = ldc;
+        g.offsets = offsets;
+        g.E = n_experts;
+        return i8_gemm_enqueue(g, static_cast<hipStream_t>(stream));
     })
 }
 

@@ -10,14 +10,15 @@
 // 16384 2.2 us each, a launch.
 #include "c3_internal.h"
 #include "pieces.h"
+#include "row_io.h"
 
 #include <type_traits>
 
 namespace {
 
+using namespace c3::row_io;
+
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
@@ -36,32 +37,6 @@ __device__ __noinline__ uint32_t tiny_code(float x) {
     const uint32_t c = (uint32_t)(a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) +
                        (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
     return c | ((__builtin_bit_cast(uint32_t, x) >> 28) & 8u);
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
-
-// Eight values in the type they come in: fp32 in eight words, bf16 in four.
-template <bool BF16>
-struct Eight {
-    uint32_t w[BF16 ? 4 : 8];
-};
-
-// Bits of the largest magnitude, as fp32.
-template <bool BF16>
-__device__ __forceinline__ uint32_t largest(const Eight<BF16>& x) {
-    if constexpr (BF16) {
-        u16x2_t m = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, x.w[i] & 0x7FFF7FFFu));
-        return (uint32_t)max(m.x, m.y) << 16;
-    } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, x.w[i] & 0x7FFFFFFFu);
-        return m;
-    }
 }
 
 // The codes of eight values of a block with this scale byte, the first in the low nibble.
@@ -93,33 +68,6 @@ __device__ __forceinline__ uint32_t encode(const Eight<BF16>& x, uint32_t byte) 
         c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f(6), f(7), s, 3);
     }
     return byte == 255u ? 0u : c;
-}
-
-// Eight values at p, of which `fit` belong to the row (the rest are zero). Whole pieces are two
-// or one 16-byte loads whatever the alignment; x is read once (non-temporal).
-template <bool BF16>
-__device__ __forceinline__ Eight<BF16> load_eight(const char* p, int64_t fit) {
-    typedef u32x4_t loose __attribute__((aligned(2)));
-    Eight<BF16> x;
-    if (fit >= 8) {
-#pragma unroll
-        for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
-            const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const loose*>(p) + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x.w[4 * i + j] = v[j];
-        }
-    } else if constexpr (BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = 2 * i < fit ? reinterpret_cast<const uint16_t*>(p)[2 * i] : 0;
-            const uint32_t hi = 2 * i + 1 < fit ? reinterpret_cast<const uint16_t*>(p)[2 * i + 1] : 0;
-            x.w[i] = lo | hi << 16;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x.w[i] = i < fit ? reinterpret_cast<const uint32_t*>(p)[i] : 0;
-    }
-    return x;
 }
 
 constexpr int kThreads = 256;
@@ -323,15 +271,6 @@ __global__ __launch_bounds__(kThreads) void dequantize_rows(const void* __restri
 
 namespace c3 {
 
-// Rows [r, r + n) at a time, up to `most` of them: one launch takes below 2^32 threads.
-template <typename Launch>
-static c3_status in_parts(int64_t rows, int64_t most, Launch launch) {
-    for (int64_t r = 0; r < rows; r += most) {
-        launch(r, std::min(most, rows - r));
-        C3_HIP_TRY(hipGetLastError());
-    }
-    return C3_OK;
-}
 // Workgroups of a launch, and rows of `per_row` pieces that they take (per_row < 2^29).
 constexpr int64_t kMostGroups = (int64_t(1) << 32) / kThreads - 1;
 static int64_t most_rows(uint32_t per_row) { return kMostGroups * kThreads * kPieces / per_row; }

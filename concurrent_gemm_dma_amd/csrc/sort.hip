@@ -1,0 +1,234 @@
+// sort.hip -- rows sorted by expert and back: y[p] = x[order[p] % T], out[t] = sum over choices j of
+// w[t][j] * y[pos[j * T + t]], and the gradients of that sum.
+//
+// All of it is bound by memory: a row per token and one per slot (two in the gradient). Lanes take
+// 16-byte pieces of rows, counted over all rows of the launch, so that rows of any length fill the
+// lanes; a lane finds its row's places itself (lanes of one row read the same word).
+#include "c3_internal.h"
+#include "pieces.h"
+#include "row_io.h"
+
+namespace {
+
+using namespace c3::row_io;
+using c3::At;
+using c3::locate;
+
+constexpr int kThreads = 256;
+
+// Places of slots, T tokens of top_k choices. S = T * top_k.
+struct Plan {
+    const int32_t *order, *offsets;
+    int32_t* pos;
+    int T, top_k, E, S;
+};
+
+// Rows that belong to an expert, whatever offsets holds.
+__device__ __forceinline__ int present(const Plan& g) { return min(max(g.offsets[g.E], 0), g.S); }
+
+// A lane copies a piece of sorted row p: every row is read again for each choice that has it, but
+// one launch does it all.
+template <int SIZE>
+__global__ __launch_bounds__(kThreads) void dispatch_by_row(const Plan g, int64_t first_row, int64_t rows,
+                                                            const char* __restrict__ x, int64_t ld_x,
+                                                            char* __restrict__ y, int64_t ld_y, int64_t cols,
+                                                            uint32_t per_row, uint32_t magic) {
+    const At at = locate((int64_t)blockIdx.x * kThreads, threadIdx.x, per_row, magic);
+    if (at.row >= rows) return;
+    const int p = (int)(first_row + at.row), slot = g.order[p], n = present(g);
+    if (slot < 0 || slot >= g.S) return;
+    if (at.piece == 0) g.pos[slot] = p < n ? p : -1;
+    if (p >= n) return;
+    const int64_t c = (int64_t)at.piece * kValues<SIZE>;
+    const u32x4_t v = load_piece<SIZE, false>(x + ((int64_t)(slot % g.T) * ld_x + c) * SIZE, cols - c);
+    store_piece<SIZE, false>(y + ((int64_t)p * ld_y + c) * SIZE, v, cols - c);
+}
+
+__global__ __launch_bounds__(kThreads) void positions(const Plan g) {
+    const int64_t p = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (p >= g.S) return;
+    const int slot = g.order[p];
+    if (slot >= 0 && slot < g.S) g.pos[slot] = p < present(g) ? (int)p : -1;
+}
+
+// A lane copies a piece of token t to each of its rows: x is read once.
+template <int SIZE>
+__global__ __launch_bounds__(kThreads) void dispatch_by_token(const Plan g, int64_t first_row, int64_t rows,
+                                                              const char* __restrict__ x, int64_t ld_x,
+                                                              char* __restrict__ y, int64_t ld_y, int64_t cols,
+                                                              uint32_t per_row, uint32_t magic) {
+    const At at = locate((int64_t)blockIdx.x * kThreads, threadIdx.x, per_row, magic);
+    if (at.row >= rows) return;
+    const int64_t t = first_row + at.row, c = (int64_t)at.piece * kValues<SIZE>;
+    const int n = present(g);
+    const u32x4_t v = load_piece<SIZE, true>(x + (t * ld_x + c) * SIZE, cols - c);
+    for (int j = 0; j < g.top_k; ++j) {
+        const int p = g.pos[(int64_t)j * g.T + t];
+        if (p >= 0 && p < n) store_piece<SIZE, true>(y + ((int64_t)p * ld_y + c) * SIZE, v, cols - c);
+    }
+}
+
+// A lane adds a piece of out[t] up, B choices' loads in flight together.
+template <int SIZE, int B>
+__global__ __launch_bounds__(kThreads) void combine_rows(const Plan g, int64_t first_row, int64_t rows,
+                                                         const char* __restrict__ y, int64_t ld_y,
+                                                         const float* __restrict__ weights,
+                                                         char* __restrict__ out, int64_t ld_out, int64_t cols,
+                                                         uint32_t per_row, uint32_t magic) {
+    constexpr int V = kValues<SIZE>;
+    const At at = locate((int64_t)blockIdx.x * kThreads, threadIdx.x, per_row, magic);
+    if (at.row >= rows) return;
+    const int64_t t = first_row + at.row, c = (int64_t)at.piece * V;
+    float acc[V] = {};
+    for (int j0 = 0; j0 < g.top_k; j0 += B) {
+        int p[B];
+        float w[B];
+        u32x4_t v[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            p[b] = j0 + b < g.top_k ? g.pos[(int64_t)(j0 + b) * g.T + t] : -1;
+            w[b] = weights && j0 + b < g.top_k ? weights[t * g.top_k + j0 + b] : 1.f;
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (p[b] >= 0 && p[b] < g.S) v[b] = load_piece<SIZE, true>(y + ((int64_t)p[b] * ld_y + c) * SIZE, cols - c);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (p[b] >= 0 && p[b] < g.S)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(w[b], value_of<SIZE>(v[b], i), acc[i]);
+    }
+    store_piece<SIZE, true>(out + (t * ld_out + c) * SIZE, piece_of<SIZE>(acc), cols - c);
+}
+
+// G lanes take a choice of a token: its row's gradient, and the product of the token's gradient with
+// its row, added up in a fixed order.
+template <int SIZE, int G>
+__global__ __launch_bounds__(G > kThreads ? G : kThreads) void combine_gradient(
+    const Plan g, int64_t first_pair, int64_t pairs, const char* __restrict__ dout, int64_t ld_d,
+    const char* __restrict__ y, int64_t ld_y, const float* __restrict__ weights, char* __restrict__ dy,
+    int64_t ld_dy, float* __restrict__ dweights, int64_t cols) {
+    constexpr int V = kValues<SIZE>, PER = G > kThreads ? 1 : kThreads / G, U = 4;
+    const int lane = threadIdx.x % G;
+    const int64_t i = (int64_t)blockIdx.x * PER + threadIdx.x / G;
+    if (i >= pairs) return;  // whole groups, and whole workgroups where a group has several waves
+    const int64_t pair = first_pair + i, t = pair / g.top_k;
+    const int p = g.pos[(pair - t * g.top_k) * g.T + t];
+    const bool here = p >= 0 && p < g.S;
+    float sum = 0.f;
+    if (here) {
+        const float w = weights ? weights[pair] : 1.f;
+        const char *d = dout + t * ld_d * SIZE, *r = y + (int64_t)p * ld_y * SIZE;
+        char* o = dy + (int64_t)p * ld_dy * SIZE;
+        for (int64_t c0 = (int64_t)lane * V; c0 < cols; c0 += (int64_t)U * G * V) {
+            u32x4_t a[U], b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + (int64_t)u * G * V;
+                a[u] = b[u] = u32x4_t{};
+                if (c >= cols) continue;
+                a[u] = load_piece<SIZE, false>(d + c * SIZE, cols - c);
+                if (dweights) b[u] = load_piece<SIZE, true>(r + c * SIZE, cols - c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + (int64_t)u * G * V;
+                if (c >= cols) continue;
+                float f[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    f[e] = w * value_of<SIZE>(a[u], e);
+                    sum = fmaf(value_of<SIZE>(a[u], e), value_of<SIZE>(b[u], e), sum);
+                }
+                store_piece<SIZE, true>(o + c * SIZE, piece_of<SIZE>(f), cols - c);
+            }
+        }
+    }
+    if (!dweights) return;
+#pragma unroll
+    for (int m = 1; m < (G < 64 ? G : 64); m <<= 1) sum += __shfl_xor(sum, m);
+    if constexpr (G > 64) {
+        __shared__ float part[kThreads / 64 > G / 64 ? kThreads / 64 : G / 64];
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+        __syncthreads();
+        if (lane == 0) {
+            sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < G / 64; ++v) sum += part[threadIdx.x / 64 + v];
+        }
+    }
+    if (lane == 0) dweights[pair] = here ? sum : 0.f;
+}
+
+Plan plan_of(const c3::SortArgs& a) {
+    return {a.order, a.offsets, a.pos, (int)a.T, a.top_k, a.E, (int)(a.T * a.top_k)};
+}
+
+// Rows of `per_row` pieces that one launch takes (per_row < 2^29).
+constexpr int64_t kMostGroups = (int64_t(1) << 32) / kThreads - 1;
+int64_t most_rows(uint32_t per_row) { return std::max<int64_t>(1, kMostGroups * kThreads / per_row); }
+dim3 groups_of(int64_t rows, uint32_t per_row) {
+    return dim3((unsigned)((rows * per_row + kThreads - 1) / kThreads));
+}
+
+template <int SIZE>
+uint32_t pieces_of(int64_t cols) { return (uint32_t)((cols + kValues<SIZE> - 1) / kValues<SIZE>); }
+
+template <int SIZE>
+c3_status dispatch(const c3::SortArgs& a, hipStream_t stream) {
+    const Plan g = plan_of(a);
+    const uint32_t per_row = pieces_of<SIZE>(a.cols), magic = c3::magic_of(per_row);
+    const char* x = static_cast<const char*>(a.x);
+    char* y = static_cast<char*>(a.out);
+    return c3::in_parts(g.S, most_rows(per_row), [&](int64_t r, int64_t n) {
+        hipLaunchKernelGGL(dispatch_by_row<SIZE>, groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n, x,
+                           a.ld_x, y, a.ld_out, a.cols, per_row, magic);
+    });
+}
+
+template <int SIZE>
+c3_status combine(const c3::SortArgs& a, hipStream_t stream) {
+    const Plan g = plan_of(a);
+    const uint32_t per_row = pieces_of<SIZE>(a.cols), magic = c3::magic_of(per_row);
+    return c3::in_parts(a.T, most_rows(per_row), [&](int64_t r, int64_t n) {
+        hipLaunchKernelGGL((combine_rows<SIZE, 4>), groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n,
+                           static_cast<const char*>(a.y), a.ld_y, a.weights, static_cast<char*>(a.out), a.ld_out,
+                           a.cols, per_row, magic);
+    });
+}
+
+template <int SIZE, int G>
+c3_status launch_gradient(const c3::SortArgs& a, hipStream_t stream) {
+    constexpr int threads = std::max(G, kThreads), per = threads / G;
+    const Plan g = plan_of(a);
+    return c3::in_parts(g.S, ((int64_t(1) << 32) / threads - 1) * per, [&](int64_t r, int64_t n) {
+        hipLaunchKernelGGL((combine_gradient<SIZE, G>), dim3((unsigned)((n + per - 1) / per)), dim3(threads), 0,
+                           stream, g, r, n, static_cast<const char*>(a.x), a.ld_x, static_cast<const char*>(a.y),
+                           a.ld_y, a.weights, static_cast<char*>(a.out), a.ld_out, a.dweights, a.cols);
+    });
+}
+
+}  // namespace
+
+namespace c3 {
+
+c3_status positions_enqueue(const SortArgs& a, hipStream_t stream) {
+    const Plan g = plan_of(a);
+    hipLaunchKernelGGL(positions, dim3((unsigned)(((int64_t)g.S + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, g);
+    C3_HIP_TRY(hipGetLastError());
+    return C3_OK;
+}
+
+c3_status dispatch_enqueue(const SortArgs& a, hipStream_t stream) {
+    return a.dtype == C3_BF16 ? dispatch<2>(a, stream) : dispatch<4>(a, stream);
+}
+
+c3_status combine_enqueue(const SortArgs& a, hipStream_t stream) {
+    return a.dtype == C3_BF16 ? combine<2>(a, stream) : combine<4>(a, stream);
+}
+
+c3_status combine_backward_enqueue(const SortArgs& a, hipStream_t stream) {
+    return a.dtype == C3_BF16 ? launch_gradient<2, 64>(a, stream) : launch_gradient<4, 64>(a, stream);
+}
+
+}  // namespace c3

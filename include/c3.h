@@ -37,7 +37,7 @@
 extern "C" {
 #endif
 
-#define C3_ABI_VERSION 6
+#define C3_ABI_VERSION 7
 #define C3_MAX_MASK_WORDS 8 /* CU masks cover up to 256 CUs, bit i = CU i as the driver numbers it */
 #define C3_MAX_SEGMENTS 4096
 #define C3_MAX_WORLD 64 /* ranks of a reduce-scatter / all-reduce local share */
@@ -487,6 +487,92 @@ c3_status c3_mx4_gemm_experts(const void* A, const void* sA, int64_t a_rows, con
                               const float* weights, void* C, c3_dtype dtype, int64_t n_tokens,
                               int top_k, int n_experts, int64_t N, int64_t K, int64_t ldc,
                               void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Tokens to their experts and back, and expert layers in 8-bit integers: the buffers on both sides
+ * of an expert layer's all-to-alls, and what is computed between them on rows sorted by expert.
+ * Slots, order and offsets are c3_route_plan's; n = offsets[n_experts] slots have an expert.
+ *
+ * int8 operand of `rows` x `cols`: with P = cols rounded up to a multiple of C3_I8_PAD,
+ * codes[rows][P] (signed bytes, zeros past cols; 16-byte aligned) and scales[rows] fp32; a code c
+ * of row i stands for c * scales[i]. c3_i8_bytes gives the sizes of both arrays.
+ *
+ * Every call here is stream-ordered, asynchronous and deterministic (no atomics, fixed summation
+ * order), allocates nothing and may be captured into a graph. Buffers a call writes must not
+ * overlap those it reads or other ones it writes (C3_E_OVERLAP). Matrices may have any element
+ * alignment; what is past cols in a row is left alone. Row strides and cols are below 2^31,
+ * n_tokens * top_k (the number of slots) too. order, offsets and pos are read on the device only:
+ * entries outside their ranges are skipped, never followed.
+ * ------------------------------------------------------------------------------------------- */
+
+#define C3_I8_PAD 128
+#define C3_I8_MAX_K 131071 /* 128 * 128 * K stays below 2^31 */
+
+/* Sort rows by expert, the send buffer of an all-to-all: y[p] = x[order[p] % n_tokens] for p < n.
+ * x[n_tokens][ld], y[n_tokens * top_k][ld_y] (dtype); rows n.. of y are left as they were.
+ * pos[n_tokens * top_k]: slot s is row pos[s] of y, or -1 without an expert: what c3_combine reads.
+ * Where order is not c3_route_plan's, slots it does not name keep their old pos.
+ * Its gradient is c3_combine without weights. n_tokens = 0 is a no-op; cols >= 1. */
+c3_status c3_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_t cols, int64_t ld,
+                      const int32_t* order, const int32_t* offsets, int top_k, int n_experts,
+                      void* y, int64_t ld_y, int32_t* pos, void* stream);
+
+/* The way back: out[t] = sum over j < top_k of weights[t][j] * y[pos[j * n_tokens + t]], choices
+ * whose pos is outside [0, n_tokens * top_k) left out (out is 0 without any). fp32, added in the
+ * order of j, rounded once to dtype. weights[n_tokens][top_k] fp32, NULL = 1. y has n_tokens *
+ * top_k rows of ld_y, of which only those that pos names are read; out[n_tokens][ld_out]. */
+c3_status c3_combine(const void* y, c3_dtype dtype, int64_t n_tokens, int top_k, int64_t cols,
+                     int64_t ld_y, const int32_t* pos, const float* weights, void* out,
+                     int64_t ld_out, void* stream);
+
+/* Gradients of c3_combine from dout[n_tokens][ld_d]: for every slot s = j * n_tokens + t with a row
+ *     dy[pos[s]] = weights[t][j] * dout[t]        (dtype, rounded once; other rows are left alone)
+ *     dweights[t][j] = sum over c of dout[t][c] * y[pos[s]][c]       (fp32 sums; 0 without a row)
+ * weights NULL = 1. dweights may be NULL, then y is not read and may be NULL too. No two slots may
+ * have the same row, as none have in c3_dispatch's pos. */
+c3_status c3_combine_backward(const void* dout, c3_dtype dtype, int64_t n_tokens, int top_k,
+                              int64_t cols, int64_t ld_d, const void* y, int64_t ld_y,
+                              const int32_t* pos, const float* weights, void* dy, int64_t ld_dy,
+                              float* dweights, void* stream);
+
+/* Sizes of the two arrays of an int8 operand (host arithmetic only; either pointer may be NULL).
+ * 0 <= rows < 2^31, 1 <= cols < 2^31. */
+c3_status c3_i8_bytes(int64_t rows, int64_t cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Quantise x[rows][ld] (dtype) to the int8 operand of rows x cols. With a = the row's largest
+ * magnitude, at least 2^-119: scale = a / 127, codes x * r rounded to the nearest integer, ties to
+ * even, r = 127 / a rounded to fp32 (so codes are in -127 .. 127). A row with an infinity or NaN gets
+ * scale NaN and codes 0. rows = 0 is a no-op; cols >= 1; rows below 2^31. */
+c3_status c3_i8_quantize(const void* x, c3_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                         void* codes, float* scales, void* stream);
+
+/* c3_dispatch of quantised rows: the int8 operand of n_tokens * top_k rows in which row p < n is
+ * x[order[p] % n_tokens], quantised by c3_i8_quantize's rule: half the bytes of bf16 for the
+ * all-to-all, and the rows that c3_i8_gemm_experts multiplies. Rows n.. are left as they were. */
+c3_status c3_i8_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_t cols, int64_t ld,
+                         const int32_t* order, const int32_t* offsets, int top_k, int n_experts,
+                         void* codes, float* scales, int32_t* pos, void* stream);
+
+/* The values of an int8 operand of rows x cols: y[rows][ld] (dtype), code * scale in fp32, rounded
+ * to dtype. */
+c3_status c3_i8_dequantize(const void* codes, const float* scales, int64_t rows, int64_t cols,
+                           void* y, c3_dtype dtype, int64_t ld, void* stream);
+
+/* C[M][ldc] = A . B^T for int8 operands A (M x K, a scale for each row of C) and B (N x K, a scale
+ * for each column): exact int32 sums, times sA[m], times sB[n] in fp32, rounded to dtype.
+ * M = 0 or N = 0 is a no-op; M, N <= 2^21, 1 <= K <= C3_I8_MAX_K. */
+c3_status c3_i8_gemm(const void* A, const float* sA, const void* B, const float* sB, void* C,
+                     c3_dtype dtype, int64_t M, int64_t N, int64_t K, int64_t ldc, void* stream);
+
+/* Every expert's product on rows sorted by expert (c3_dispatch's order, or what an all-to-all
+ * delivers): C[p] = A[p] . B[e]^T as c3_i8_gemm for p in [offsets[e], offsets[e + 1]); rows of no
+ * expert are left as they were. A is an operand of n_rows x K, B one of (n_experts * N) x K, expert
+ * e's N rows starting at row e * N, C has n_rows rows of ldc >= N; offsets[n_experts + 1] is
+ * ascending. n_rows = 0 or N = 0 is a no-op; n_rows <= 2^24, N <= 2^21, 1 <= K <= C3_I8_MAX_K,
+ * n_experts <= C3_MAX_EXPERTS. */
+c3_status c3_i8_gemm_experts(const void* A, const float* sA, const void* B, const float* sB,
+                             const int32_t* offsets, void* C, c3_dtype dtype, int64_t n_rows,
+                             int n_experts, int64_t N, int64_t K, int64_t ldc, void* stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Concurrent run (C3)
