@@ -11,13 +11,17 @@
 // Rows past M or N read a valid row instead (their results are not stored); columns need no mask,
 // since operands are padded with zeros to a multiple of 128.
 #include "c3_internal.h"
+#include "tile_util.h"
 
 #include <cmath>
-#include <type_traits>
 
 namespace {
 
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
+using namespace c3::tile;
+
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 // What the kernels read (one struct argument).
 struct Args {
@@ -35,111 +39,387 @@ struct Rows {
     int begin, end, expert;
 };
 
+// What 64 experts, one a lane, own of the rows, in tiles of BM. Offsets are clamped to the rows that
+// there are, so whatever they hold nothing outside them is read or written.
+template <int BM>
+struct Share {
+    int lo = 0, hi = 0, tiles, sum, total;  // sum: of the tiles up to this lane's
+    __device__ __forceinline__ Share(const Args& g, int e) {
+        if (e < g.E) {
+            lo = min(max(g.offsets[e], 0), g.M);
+            hi = min(max(g.offsets[e + 1], lo), g.M);
+        }
+        tiles = sum = (hi - lo + BM - 1) / BM;
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(sum, d);
+            if (lane >= d) sum += up;
+        }
+        total = __builtin_amdgcn_readlane(sum, 63);
+    }
+    // tile t < total of these, the first expert being e0
+    __device__ __forceinline__ Rows pick(int t, int e0) const {
+        const int f = __builtin_ctzll(__ballot(sum > t));
+        const int begin = __builtin_amdgcn_readlane(lo, f) + (t - __builtin_amdgcn_readlane(sum - tiles, f)) * BM;
+        return {begin, min(__builtin_amdgcn_readlane(hi, f), begin + BM), e0 + f};
+    }
+};
+
 // Tile t of BM rows, counted over the experts in turn, each expert's range cut into tiles of its
-// own. Offsets are clamped to the rows that there are. false past the last tile.
+// own. false past the last tile.
 template <int BM>
 __device__ __forceinline__ bool find_rows(const Args& g, int t, Rows& r) {
     if (!g.offsets) {
         r = {t * BM, min(g.M, t * BM + BM), 0};
         return t * BM < g.M;
     }
-    const int lane = threadIdx.x & 63;
     int base = 0;
     for (int e0 = 0; e0 < g.E; e0 += 64) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < g.E) {
-            lo = min(max(g.offsets[e], 0), g.M);
-            hi = min(max(g.offsets[e + 1], lo), g.M);
-        }
-        const int tiles = (hi - lo + BM - 1) / BM;
-        int sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
-        const int total = __builtin_amdgcn_readlane(sum, 63);
-        if (t < base + total) {
-            const int f = __builtin_ctzll(__ballot(sum > t - base));
-            const int begin = __builtin_amdgcn_readlane(lo, f) + (t - base - __builtin_amdgcn_readlane(sum - tiles, f)) * BM;
-            r = {begin, min(__builtin_amdgcn_readlane(hi, f), begin + BM), e0 + f};
+        const Share<BM> s(g, e0 + (threadIdx.x & 63));
+        if (t < base + s.total) {
+            r = s.pick(t - base, e0);
             return true;
         }
-        base += total;
+        base += s.total;
     }
     return false;
+}
+
+// Tiles of BM rows; no more than the grid was made for, whatever the offsets hold.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const Args& g) {
+    if (!g.offsets) return (g.M + BM - 1) / BM;
+    int n = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 64) n += Share<BM>(g, e0 + (threadIdx.x & 63)).total;
+    return min(n, g.M / BM + min(g.E, g.M));
 }
 
 // ------------------------------------------------------------------------------------------------
 // Few rows
 // ------------------------------------------------------------------------------------------------
-// A workgroup computes 16*MT rows x 16*NT columns of C; its waves (1 to 16) take the 256-column
-// chunks of K in turn and add their sums up through LDS, so K is split over a workgroup without a
-// workspace. Operands go straight to registers: load j of a chunk takes 16 bytes at 64 * j + 16 *
-// (l / 16) of row l % 16 (64 contiguous bytes of each row), which is the lane's operand of matrix
-// instruction j.
-template <int I>
-using Int = std::integral_constant<int, I>;
-
-template <int MT, int NT>
-__global__ __launch_bounds__(MT * NT == 4 ? 1024 : 512) void i8_gemm_rows(const Args g) {
-    constexpr int BM = 16 * MT, BN = 16 * NT, TILE = BM * BN;
-    extern __shared__ int sums[];  // [waves][BM][BN]
+// A workgroup computes BM rows x 16*NT columns of C; its W waves take the stages of 128 columns of K
+// in turn and add their sums up through LDS, so K is split over a workgroup without a workspace.
+// Every wave keeps two stages of its own in LDS, loaded as whole lines and read back in the layout of
+// the matrix instruction (lane l: row l % 16, 16 bytes of a 64-column step): no wave waits for
+// another one before the end.
+//
+// Bound by B's bytes where rows are few. Workgroups start at different stages of K (sums of integers
+// have no order): rows a power of two apart put one column into few memory channels, and all
+// workgroups in step would ask for that column at one time.
+template <int BM, int NT, int W>
+__global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
+    constexpr int MT = BM / 16, BN = 16 * NT, TILE = BM * BN, STAGE = (BM + BN) * 128, LOADS = (BM + BN) / 8;
+    __shared__ __attribute__((aligned(1024))) char smem[W * 2 * STAGE];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tiles_n = (g.N + BN - 1) / BN;
     Rows r;
     if (!find_rows<BM>(g, blockIdx.x / tiles_n, r)) return;
+    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
+    r.end = __builtin_amdgcn_readfirstlane(r.end);
+    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
     const int n0 = (blockIdx.x % tiles_n) * BN;
-    i32x4_t acc[MT][NT] = {};
-    const int8_t *pa[MT], *pb[NT];
+    const size_t b_base = (size_t)r.expert * g.N + n0;
+    const uint32_t row = (uint32_t)g.P;
+    const i32x4_t rA = rsrc_of(g.A + (size_t)r.begin * row), rB = rsrc_of(g.B + b_base * row);
+    // load f of a stage: rows 8 * f + lane / 8 of B, then of A
+    uint32_t at[LOADS];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) pa[m] = g.A + (size_t)min(r.begin + m * 16 + i, r.end - 1) * g.P + q * 16;
+    for (int f = 0; f < LOADS; ++f) {
+        const int n = 8 * f + (lane >> 3);
+        const uint32_t from = f < BN / 8 ? (uint32_t)min(n, g.N - 1 - n0) : (uint32_t)min(n - BN, r.end - 1 - r.begin);
+        at[f] = from * row + (uint32_t)((lane & 7) ^ swizzle(n)) * 16u;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(C3_LDS char*)smem + (uint32_t)(wave * 2 * STAGE);
+    const int nk = row / 128, mine = (nk - wave + W - 1) / W;  // stages of all waves and of this one
+    const int first = (int)(blockIdx.x % (unsigned)nk);
+    auto load = [&](int s) {  // into buffer s % 2
+        int k = wave + s * W + first;
+        if (k >= nk) k -= nk;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-        pb[n] = g.B + ((size_t)r.expert * g.N + min(n0 + n * 16 + i, g.N - 1)) * g.P + q * 16;
-    // J steps of 64 columns, all of their loads before the first use
-    auto chunk = [&](int c, auto j_c) {
-        constexpr int J = decltype(j_c)::value;
-        i32x4_t a[MT][J], b[NT][J];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < J; ++j) b[n][j] = *reinterpret_cast<const i32x4_t*>(pb[n] + (size_t)c * 256 + j * 64);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < J; ++j) a[m][j] = *reinterpret_cast<const i32x4_t*>(pa[m] + (size_t)c * 256 + j * 64);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < J; ++j)
-                    acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[n][j], a[m][j], acc[m][n], 0, 0, 0);
+        for (int f = 0; f < LOADS; ++f)
+            lds_load(f < BN / 8 ? rB : rA, lds0 + (uint32_t)((s & 1) * STAGE + f * 1024), at[f], (uint32_t)k * 128u);
     };
-    const int whole = g.P / 256;
-    for (int c = wave; c < whole; c += waves) chunk(c, Int<4>{});
-    // the last chunk may have 128 columns only
-    if ((g.P & 255) && whole % waves == wave) chunk(whole, Int<2>{});
+    i32x4_t acc[MT][NT] = {};
+    auto multiply = [&](int s) {
+        const C3_LDS char* p = (const C3_LDS char*)smem + (wave * 2 + (s & 1)) * STAGE + i * 128;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = ((4 * j + q) ^ swizzle(i)) * 16;
+            i32x4_t a[MT], b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = *reinterpret_cast<const C3_LDS i32x4_t*>(p + n * 2048 + c);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) a[m] = *reinterpret_cast<const C3_LDS i32x4_t*>(p + BN * 128 + m * 2048 + c);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[n], a[m], acc[m][n], 0, 0, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer has been read
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (mine > 0) load(0);
+    for (int s = 0; s < mine; ++s) {
+        if (s + 1 < mine) {
+            load(s + 1);
+            C3_WAIT_VMCNT(LOADS);
+        } else {
+            C3_WAIT_VMCNT(0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s);
+    }
+    __syncthreads();
     // lane holds columns 16 n + 4 q + v of row 16 m + i
+    int* sums = reinterpret_cast<int*>(smem);  // [W][BM][BN]
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             *reinterpret_cast<i32x4_t*>(&sums[wave * TILE + (m * 16 + i) * BN + n * 16 + 4 * q]) = acc[m][n];
     __syncthreads();
-    for (int e = tid; e < TILE; e += blockDim.x) {
+    for (int e = tid; e < TILE; e += 64 * W) {
         const int m = r.begin + e / BN, n = n0 + e % BN;
         if (m >= r.end || n >= g.N) continue;
         int sum = sums[e];
-        for (int w = 1; w < waves; ++w) sum += sums[w * TILE + e];
-        const float y = (float)sum * g.sA[m] * g.sB[(size_t)r.expert * g.N + n];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += sums[w * TILE + e];
+        const float y = (float)sum * g.sA[m] * g.sB[b_base + e % BN];
         const size_t o = (size_t)m * g.ldc + n;
         if (g.f32) static_cast<float*>(g.C)[o] = y;
         else static_cast<__bf16*>(g.C)[o] = static_cast<__bf16>(y);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Tile kernel
+// ------------------------------------------------------------------------------------------------
+// 4 waves (2 x 2), each 32*TM x 32*TN of C from v_mfma_i32_32x32x32_i8 (lane l: row l % 32, 16 of
+// the slice's 32 columns). K goes in stages of 128 columns: a whole line of a row. BUFS stages are
+// in LDS. A stage is four slices of TM*TN matrix instructions, one barrier before the last. While
+// those of one slice run, the wave reads the next slice's fragments; in the last and the next
+// stage's first it issues the loads that refill the buffer, one each GAP instructions.
+//
+// No load leaves its array: rows past the tile's are clamped to its last one, stages past the last
+// one load the last one again into a buffer nobody reads.
+template <int TM, int TN, int BUFS>
+__global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gemm_tile(const Args g) {
+    constexpr int BM = 64 * TM, BN = 64 * TN, ROWS = BM + BN;
+    constexpr int STAGE = ROWS * 128, SCALES = BUFS * STAGE;
+    constexpr int NM = TM * TN, NF = TM + TN;  // matrix instructions of a slice, fragments
+    constexpr int LOADS = 2 * (TM + TN);       // loads of a wave and stage
+    constexpr int GAP = 2 * NM / LOADS;        // matrix instructions between two of them
+    __shared__ __attribute__((aligned(1024))) char smem[SCALES + ROWS * 4];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int tiles_n = (g.N + BN - 1) / BN;
+    int tm, tn;
+    Rows r;
+    if (g.offsets && g.E <= 64) {  // one look at the offsets gives both
+        const Share<BM> s(g, lane);
+        const int tiles_m = min(s.total, g.M / BM + min(g.E, g.M));
+        if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+        map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        r = s.pick(__builtin_amdgcn_readfirstlane(tm), 0);
+    } else {
+        const int tiles_m = count_tiles<BM>(g);
+        if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+        map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        if (!find_rows<BM>(g, tm, r)) return;
+    }
+    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
+    r.end = __builtin_amdgcn_readfirstlane(r.end);
+    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
+    const int n0 = tn * BN;
+    const int half = lane >> 5, row32 = lane & 31;
+    const size_t b_base = (size_t)r.expert * g.N + n0;
+    auto a_row = [&](int i) -> uint32_t { return (uint32_t)min(i, r.end - 1 - r.begin); };
+    auto b_row = [&](int i) -> uint32_t { return (uint32_t)min(i, g.N - 1 - n0); };
+
+    // scales of the tile's rows and columns
+    float* scales = reinterpret_cast<float*>(smem + SCALES);
+    if (tid < BM) scales[tid] = g.sA[r.begin + a_row(tid)];
+    if (tid < BN) scales[BM + tid] = g.sB[b_base + b_row(tid)];
+
+    i32x16_t acc[TM][TN];
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni) acc[mi][ni] = i32x16_t{};
+
+    {
+        const uint32_t row = (uint32_t)g.P, nk = row / 128;
+        const i32x4_t rA = rsrc_of(g.A + (size_t)r.begin * row), rB = rsrc_of(g.B + b_base * row);
+        // load i of wave w: rows 8 * (2 * T * w + i) + lane / 8, chunk lane % 8
+        uint32_t va[2 * TM], vb[2 * TN];
+        const int q = lane >> 3;
+#pragma unroll
+        for (int i = 0; i < 2 * TM; ++i)
+            va[i] = a_row(8 * (2 * TM * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
+#pragma unroll
+        for (int i = 0; i < 2 * TN; ++i)
+            vb[i] = b_row(8 * (2 * TN * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
+        const uint32_t lds0 = (uint32_t)(uintptr_t)(C3_LDS char*)smem;
+        auto load = [&](uint32_t stage, int buf, int i) {  // load i of a stage into a buffer
+            const uint32_t soff = min(stage, nk - 1) * 128u;
+            const uint32_t at = lds0 + (uint32_t)(buf * STAGE);
+            if (i < 2 * TM) lds_load(rA, at + (uint32_t)((2 * TM * wave + i) * 1024), va[i < 2 * TM ? i : 0], soff);
+            else lds_load(rB, at + (uint32_t)(BM * 128 + (2 * TN * wave + i - 2 * TM) * 1024), vb[i < 2 * TM ? 0 : i - 2 * TM], soff);
+        };
+
+        // fragment reads: f < TM of A, then of B; slice j of the half h of a stage
+        const char* lds = smem;
+        uint32_t f_at[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                f_at[h][j] = (uint32_t)row32 * 128u + (uint32_t)(((4 * h + 2 * half + j) ^ swizzle(row32)) << 4);
+        const uint32_t fa = (uint32_t)(wm * 32 * TM) * 128u, fb = (uint32_t)(BM + wn * 32 * TN) * 128u;
+        i32x4_t frag[2][NF];
+        auto read_frag = [&](int buf, int h, int j, int f) {
+            const uint32_t at = (uint32_t)(buf * STAGE) + (f < TM ? fa + f * 4096u : fb + (f - TM) * 4096u) + f_at[h][j];
+            frag[j][f] = *reinterpret_cast<const C3_LDS i32x4_t*>((const C3_LDS char*)lds + at);
+        };
+        auto mma = [&](int i, auto j_c) {
+            constexpr int J = decltype(j_c)::value;
+            const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
+            acc[mi][ni] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[J][TM + ni], frag[J][mi], acc[mi][ni], 0, 0, 0);
+        };
+        // One stage p in buffer `buf`. Its last slice and the next stage's first issue the loads of
+        // stage p + BUFS into `buf`, whose last reader finished before the barrier. When stage p + 1
+        // has to have landed, the loads of stages p + 2 .. p + BUFS - 1 may still be in flight.
+        auto stage = [&](uint32_t p, int buf) {
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                mma(i, Int<0>{});
+                if (i < NF) read_frag(buf, 0, 1, i);
+                if (i % GAP == GAP - 1) load(p + BUFS - 1, (buf + BUFS - 1) & (BUFS - 1), LOADS / 2 + i / GAP);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                mma(i, Int<1>{});
+                if (i < NF) read_frag(buf, 1, 0, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                mma(i, Int<0>{});
+                if (i < NF) read_frag(buf, 1, 1, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            C3_WAIT_VMCNT((BUFS - 2) * LOADS);
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < NM; ++i) {
+                mma(i, Int<1>{});
+                if (i < NF) read_frag((buf + 1) & (BUFS - 1), 0, 0, i);
+                if (i % GAP == 0) load(p + BUFS, buf, i / GAP);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+
+        C3_WAIT_VMCNT(0);  // the scales': what follows counts the stages' loads only
+#pragma unroll
+        for (int st = 0; st < BUFS - 1; ++st)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load(st, st, i);
+#pragma unroll
+        for (int i = 0; i < LOADS / 2; ++i) load(BUFS - 1, BUFS - 1, i);
+        C3_WAIT_VMCNT((BUFS - 2) * LOADS + LOADS / 2);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // the scales' writes
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) read_frag(0, 0, 0, f);
+        uint32_t p = 0;
+        for (; p + BUFS <= nk; p += BUFS)
+#pragma unroll
+            for (int b = 0; b < BUFS; ++b) stage(p + b, b);
+#pragma unroll
+        for (int b = 0; b < BUFS - 1; ++b)
+            if (p + b < nk) stage(p + b, b);
+        C3_WAIT_VMCNT(0);  // loads past the end still write LDS
+    }
+    __syncthreads();
+
+    // ---- C: through LDS (this wave's quarter of the stages), so that it leaves in whole 128-byte
+    // lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each 32 x 32
+    // block; a row's 16-byte chunks are permuted by its number against bank conflicts.
+    char* out = smem + wave * (SCALES / 4);
+    const int m0w = r.begin + wm * 32 * TM, nw = n0 + wn * 32 * TN;
+    auto store = [&](auto f32_c, auto full_c) {
+        constexpr bool F32 = decltype(f32_c)::value != 0;
+        constexpr bool FULL = decltype(full_c)::value != 0;  // whole 16-byte pieces only
+        constexpr int size = F32 ? 4 : 2, row_bytes = 32 * TN * size, chunks = row_bytes / 16;
+        constexpr int FIT = SCALES / 4 / (32 * row_bytes), PER = FIT < TM ? FIT : TM;  // 32-row blocks at once
+        const bool aligned = (((uintptr_t)g.C | (uint64_t)g.ldc * size) & 15) == 0;
+#pragma unroll
+        for (int m0 = 0; m0 < TM; m0 += PER) {
+#pragma unroll
+            for (int mi = m0; mi < m0 + PER; ++mi) {
+                const float sa = scales[wm * 32 * TM + mi * 32 + row32];
+#pragma unroll
+                for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+                    for (int v = 0; v < 16; v += 4) {
+                        const int n = 32 * ni + 2 * v + 4 * half;
+                        char* row = out + ((mi - m0) * 32 + row32) * row_bytes;
+                        const f32x4_t sb = *reinterpret_cast<const f32x4_t*>(&scales[BM + wn * 32 * TN + n]);
+                        f32x4_t y;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] = (float)acc[mi][ni][v + i] * sa * sb[i];
+                        if constexpr (F32) {
+                            *reinterpret_cast<f32x4_t*>(row + ((n / 4) ^ (row32 & (chunks - 1))) * 16) = y;
+                        } else {
+                            bf16x4_t b = {static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
+                                          static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
+                            *reinterpret_cast<bf16x4_t*>(row + ((n / 8) ^ (row32 & (chunks - 1))) * 16 + (n & 4) * 2) = b;
+                        }
+                    }
+            }
+            own_lds_fence();
+#pragma unroll
+            for (int u = 0; u < PER * chunks / 2; ++u) {
+                const int i = u * 64 + lane, m = i / chunks, c = i % chunks, at = m0w + m0 * 32 + m;
+                const int n = nw + c * (16 / size);
+                if (at >= r.end || (!FULL && n >= g.N)) continue;
+                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(out + m * row_bytes + (c ^ (m & (chunks - 1))) * 16);
+                char* p = static_cast<char*>(g.C) + ((size_t)at * g.ldc + n) * size;
+                const int fit = (g.N - n) * size;
+                if (FULL || (fit >= 16 && aligned)) {
+                    *reinterpret_cast<i32x4_t*>(p) = v;
+                } else if (fit >= 16) {
+                    __builtin_memcpy(__builtin_assume_aligned(p, 2), &v, 16);
+                } else if constexpr (F32) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e * 4 < fit) reinterpret_cast<int*>(p)[e] = v[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e * 2 < fit) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+                }
+            }
+            own_lds_fence();
+        }
+    };
+    const int bytes = g.f32 ? 4 : 2;
+    const bool full = nw + 32 * TN <= g.N && (((uintptr_t)g.C | (uint64_t)g.ldc * bytes) & 15) == 0;
+    if (g.f32) {
+        if (full) store(Int<1>{}, Int<1>{});
+        else store(Int<1>{}, Int<0>{});
+    } else {
+        if (full) store(Int<0>{}, Int<1>{});
+        else store(Int<0>{}, Int<0>{});
     }
 }
 
@@ -150,17 +430,60 @@ int64_t most_tiles(const c3::I8Gemm& g, int bm) {
 }
 
 // false: more workgroups than one launch takes (2^32 threads).
-template <int MT, int NT>
-bool launch_rows(const c3::I8Gemm& g, const Args& a, int n_cu, hipStream_t stream) {
-    const int64_t groups = most_tiles(g, 16 * MT) * ((g.N + 16 * NT - 1) / (16 * NT));
-    int waves = 1;
-    while (waves < (MT * NT == 4 ? 16 : 8) && 2 * waves * groups <= 24 * (int64_t)n_cu && waves * 512 < a.P)
-        waves *= 2;
-    if (groups * 64 * waves >= (int64_t(1) << 32)) return false;
-    hipLaunchKernelGGL((i8_gemm_rows<MT, NT>), dim3((unsigned)groups), dim3(64 * waves),
-                       waves * 256 * MT * NT * sizeof(int), stream, a);
+template <int BM, int NT, int W>
+bool launch_rows(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
+    const int64_t groups = most_tiles(g, BM) * ((g.N + 16 * NT - 1) / (16 * NT));
+    if (groups * 64 * W >= (int64_t(1) << 32)) return false;
+    hipLaunchKernelGGL((i8_gemm_rows<BM, NT, W>), dim3((unsigned)groups), dim3(64 * W), 0, stream, a);
     return true;
 }
+
+// false: as above.
+template <int T, int BUFS>
+bool launch_tile(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
+    constexpr int BM = 64 * T;
+    const int64_t groups = most_tiles(g, BM) * ((g.N + BM - 1) / BM);
+    if (groups * 256 >= (int64_t(1) << 32)) return false;
+    hipLaunchKernelGGL((i8_gemm_tile<T, T, BUFS>), dim3((unsigned)groups), dim3(256), 0, stream, a);
+    return true;
+}
+typedef bool (*Launch)(const c3::I8Gemm&, const Args&, hipStream_t);
+
+// What a launch would take, in us: a model of where the time goes, its constants fitted to 340 shapes
+// of 1 to 20000 rows, one matrix or up to 64 experts' (each kernel's times to within 11%, rms; what
+// it chooses is 3.4% slower than the fastest of all on average).
+struct Model {
+    const c3::I8Gemm& g;
+    double n_cu, nk, used, memory;  // stages; experts with rows; the operands' and C's bytes at 6.2 TB/s
+    Model(const c3::I8Gemm& g_, int P, int n_cu_) : g(g_), n_cu(n_cu_), nk(P / 128), used(std::min(g_.E, g_.M)) {
+        const double reached = g.offsets ? g.E * (1.0 - std::pow(1.0 - 1.0 / g.E, g.M)) : 1.0;
+        const double size = g.dtype == C3_F32 ? 4 : 2;
+        memory = (reached * g.N * P + (double)g.M * P + (double)g.M * g.N * size) / 6.2e6;
+    }
+    // Workgroups; loads of experts are not known on the host, each leaves a tile partly filled.
+    double groups(int bm, int bn) const {
+        const double m = g.offsets ? std::max(used, g.M / (double)bm + 0.6 * used) : std::ceil(g.M / (double)bm);
+        return m * std::ceil(g.N / (double)bn);
+    }
+    // Memory, the way from L2 through LDS with the matrix instructions and the sums, and the chain of a
+    // workgroup's start and stages, none of which hides the others wholly. The fullest CU counts.
+    double rows(int bm, int nt, int w) const {
+        const int bn = 16 * nt;
+        const double per_cu = std::ceil(groups(bm, bn) / n_cu), all = per_cu * n_cu;
+        const double lines = bn + std::max(2.0, std::min<double>(bm, g.M / used));
+        const double work = all * (lines * nk * 128 / 23.4e6 + bm * bn * nk * 256 / 4.06e9 + bm * bn * 2.49e-6);
+        const double rounds = std::max(1.0, per_cu / std::min(163840 / (2 * w * (bm + bn) * 128), 32 / w));
+        const double chain = rounds * (2.37 + nk / w * 0.03 * (bm + bn) / 8);
+        return 2.1 + std::sqrt(memory * memory + work * work + chain * chain);
+    }
+    // Rounds of `slots` tiles, each a fixed part and, per stage, between `low` and `high` with the share
+    // of the device that it fills.
+    double tiles(int bm, double slots, double fixed, double low, double high) const {
+        const double n = groups(bm, bm), whole = std::floor(n / slots), rest = n - whole * slots;
+        const double t = whole * (fixed + high * nk) + (rest > 0 ? fixed + (low + (high - low) * rest / slots) * nk : 0);
+        return std::sqrt(memory * memory + t * t);
+    }
+};
 
 }  // namespace
 
@@ -170,8 +493,33 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
     const Args a = {g.A, g.B, g.sA, g.sB, g.C, g.offsets, g.ldc, g.M, g.N, (int)i8_padded(g.K), g.E,
                     (int)(g.dtype == C3_F32)};
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
-    const bool few = g.offsets ? g.M <= 8 * (int64_t)std::min(g.E, g.M) : g.M <= 16;
-    if (!(few ? launch_rows<1, 2>(g, a, n_cu, stream) : launch_rows<2, 2>(g, a, n_cu, stream)))
+    const Model model(g, a.P, n_cu);
+    // 128 rows: four stages in LDS where that costs no CU its second workgroup
+    const bool alone = model.groups(128, 128) <= n_cu;
+    Launch launch = alone ? launch_tile<2, 4> : launch_tile<2, 2>;
+    double least = model.tiles(128, 2 * n_cu, 4.97, 0.28, 1.18);
+    auto consider = [&](double t, Launch l) {
+        if (t < least) {
+            least = t;
+            launch = l;
+        }
+    };
+    consider(model.tiles(256, n_cu, 11.2, 1.02, 1.67), launch_tile<4, 2>);
+    if (g.M <= 256 * (int64_t)model.used) {  // 5% off what the model says: it favours these
+        auto rows = [&](int bm, int nt, int w) { return 1.05 * model.rows(bm, nt, w); };
+        consider(rows(16, 1, 1), launch_rows<16, 1, 1>);
+        consider(rows(16, 1, 2), launch_rows<16, 1, 2>);
+        consider(rows(16, 1, 4), launch_rows<16, 1, 4>);
+        consider(rows(16, 1, 8), launch_rows<16, 1, 8>);
+        consider(rows(32, 2, 1), launch_rows<32, 2, 1>);
+        consider(rows(32, 2, 2), launch_rows<32, 2, 2>);
+        consider(rows(32, 2, 4), launch_rows<32, 2, 4>);
+        consider(rows(32, 2, 8), launch_rows<32, 2, 8>);
+        consider(rows(64, 4, 1), launch_rows<64, 4, 1>);
+        consider(rows(64, 4, 2), launch_rows<64, 4, 2>);
+        consider(rows(64, 4, 4), launch_rows<64, 4, 4>);
+    }
+    if (!launch(g, a, stream) && !launch_tile<4, 2>(g, a, stream))
         return fail(C3_E_INVALID, "int8 product: too many tiles");
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;
