@@ -215,6 +215,8 @@ struct SortArgs {
 c3_status dispatch_enqueue(const SortArgs& a, hipStream_t stream);
 c3_status combine_enqueue(const SortArgs& a, hipStream_t stream);
 c3_status combine_backward_enqueue(const SortArgs& a, hipStream_t stream);
+// Whether a dispatch is done token by token, after the positions.
+bool by_token(const SortArgs& a);
 // pos[order[p]] = p below offsets[E], -1 past it.
 c3_status positions_enqueue(const SortArgs& a, hipStream_t stream);
 

@@ -51,24 +51,33 @@ __global__ __launch_bounds__(kThreads) void positions(const Plan g) {
     if (slot >= 0 && slot < g.S) g.pos[slot] = p < present(g) ? (int)p : -1;
 }
 
-// A lane copies a piece of token t to each of its rows: x is read once.
-template <int SIZE>
+// A lane copies a piece of token t to each of its rows: x is read once. Stores go past the caches
+// (ONCE) where a token has few rows: 32768 tokens of 4096 bf16, one choice each, 92 us against 98, but
+// with eight 476 against 446 (5.4 TB/s), written lines waiting in the caches for their neighbours.
+template <int SIZE, bool ONCE>
 __global__ __launch_bounds__(kThreads) void dispatch_by_token(const Plan g, int64_t first_row, int64_t rows,
                                                               const char* __restrict__ x, int64_t ld_x,
                                                               char* __restrict__ y, int64_t ld_y, int64_t cols,
                                                               uint32_t per_row, uint32_t magic) {
+    constexpr int B = 4;  // places in flight together
     const At at = locate((int64_t)blockIdx.x * kThreads, threadIdx.x, per_row, magic);
     if (at.row >= rows) return;
     const int64_t t = first_row + at.row, c = (int64_t)at.piece * kValues<SIZE>;
     const int n = present(g);
     const u32x4_t v = load_piece<SIZE, true>(x + (t * ld_x + c) * SIZE, cols - c);
-    for (int j = 0; j < g.top_k; ++j) {
-        const int p = g.pos[(int64_t)j * g.T + t];
-        if (p >= 0 && p < n) store_piece<SIZE, true>(y + ((int64_t)p * ld_y + c) * SIZE, v, cols - c);
+    for (int j0 = 0; j0 < g.top_k; j0 += B) {
+        int p[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) p[b] = j0 + b < g.top_k ? g.pos[(int64_t)(j0 + b) * g.T + t] : -1;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (p[b] >= 0 && p[b] < n) store_piece<SIZE, ONCE>(y + ((int64_t)p[b] * ld_y + c) * SIZE, v, cols - c);
     }
 }
 
-// A lane adds a piece of out[t] up, B choices' loads in flight together.
+// A lane adds a piece of out[t] up, B choices' loads in flight together. Where memory is kept busy all
+// the same, two are enough and more lanes fit: 32768 tokens of 4096 bf16, eight choices, 406 us (5.95
+// TB/s) against 430 with four and 425 with eight; 8192 of 100, six choices, 11.8 against 10.4 and 8.9.
 template <int SIZE, int B>
 __global__ __launch_bounds__(kThreads) void combine_rows(const Plan g, int64_t first_row, int64_t rows,
                                                          const char* __restrict__ y, int64_t ld_y,
@@ -102,13 +111,15 @@ __global__ __launch_bounds__(kThreads) void combine_rows(const Plan g, int64_t f
 }
 
 // G lanes take a choice of a token: its row's gradient, and the product of the token's gradient with
-// its row, added up in a fixed order.
-template <int SIZE, int G>
+// its row, added up in a fixed order; U pieces of both in flight. The choices of a token are taken
+// next to each other, so that its gradient comes from memory about once.
+// 8192 tokens of 8192 bf16, eight choices: 418 us (5.5 TB/s) with 128 lanes, 443 with 64 and 4 pieces.
+template <int SIZE, int G, int U>
 __global__ __launch_bounds__(G > kThreads ? G : kThreads) void combine_gradient(
     const Plan g, int64_t first_pair, int64_t pairs, const char* __restrict__ dout, int64_t ld_d,
     const char* __restrict__ y, int64_t ld_y, const float* __restrict__ weights, char* __restrict__ dy,
     int64_t ld_dy, float* __restrict__ dweights, int64_t cols) {
-    constexpr int V = kValues<SIZE>, PER = G > kThreads ? 1 : kThreads / G, U = 4;
+    constexpr int V = kValues<SIZE>, PER = G > kThreads ? 1 : kThreads / G;
     const int lane = threadIdx.x % G;
     const int64_t i = (int64_t)blockIdx.x * PER + threadIdx.x / G;
     if (i >= pairs) return;  // whole groups, and whole workgroups where a group has several waves
@@ -174,15 +185,23 @@ dim3 groups_of(int64_t rows, uint32_t per_row) {
 template <int SIZE>
 uint32_t pieces_of(int64_t cols) { return (uint32_t)((cols + kValues<SIZE> - 1) / kValues<SIZE>); }
 
+// Traffic beyond the last-level cache: memory is busy all through the launch.
+constexpr double kLarge = 256e6;
+
 template <int SIZE>
 c3_status dispatch(const c3::SortArgs& a, hipStream_t stream) {
     const Plan g = plan_of(a);
     const uint32_t per_row = pieces_of<SIZE>(a.cols), magic = c3::magic_of(per_row);
     const char* x = static_cast<const char*>(a.x);
     char* y = static_cast<char*>(a.out);
-    return c3::in_parts(g.S, most_rows(per_row), [&](int64_t r, int64_t n) {
-        hipLaunchKernelGGL(dispatch_by_row<SIZE>, groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n, x,
-                           a.ld_x, y, a.ld_out, a.cols, per_row, magic);
+    const bool tokens = c3::by_token(a);
+    if (tokens) C3_TRY(c3::positions_enqueue(a, stream));
+    auto kernel = !tokens       ? dispatch_by_row<SIZE>
+                  : a.top_k > 4 ? dispatch_by_token<SIZE, false>
+                                : dispatch_by_token<SIZE, true>;
+    return c3::in_parts(tokens ? a.T : g.S, most_rows(per_row), [&](int64_t r, int64_t n) {
+        hipLaunchKernelGGL(kernel, groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n, x, a.ld_x, y, a.ld_out,
+                           a.cols, per_row, magic);
     });
 }
 
@@ -190,27 +209,54 @@ template <int SIZE>
 c3_status combine(const c3::SortArgs& a, hipStream_t stream) {
     const Plan g = plan_of(a);
     const uint32_t per_row = pieces_of<SIZE>(a.cols), magic = c3::magic_of(per_row);
+    const bool large = (double)(g.S + a.T) * a.cols * SIZE > kLarge;
+    auto kernel = a.top_k <= 4 ? combine_rows<SIZE, 4> : large ? combine_rows<SIZE, 2> : combine_rows<SIZE, 8>;
     return c3::in_parts(a.T, most_rows(per_row), [&](int64_t r, int64_t n) {
-        hipLaunchKernelGGL((combine_rows<SIZE, 4>), groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n,
+        hipLaunchKernelGGL(kernel, groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n,
                            static_cast<const char*>(a.y), a.ld_y, a.weights, static_cast<char*>(a.out), a.ld_out,
                            a.cols, per_row, magic);
     });
 }
 
-template <int SIZE, int G>
+template <int SIZE, int G, int U>
 c3_status launch_gradient(const c3::SortArgs& a, hipStream_t stream) {
     constexpr int threads = std::max(G, kThreads), per = threads / G;
     const Plan g = plan_of(a);
     return c3::in_parts(g.S, ((int64_t(1) << 32) / threads - 1) * per, [&](int64_t r, int64_t n) {
-        hipLaunchKernelGGL((combine_gradient<SIZE, G>), dim3((unsigned)((n + per - 1) / per)), dim3(threads), 0,
+        hipLaunchKernelGGL((combine_gradient<SIZE, G, U>), dim3((unsigned)((n + per - 1) / per)), dim3(threads), 0,
                            stream, g, r, n, static_cast<const char*>(a.x), a.ld_x, static_cast<const char*>(a.y),
                            a.ld_y, a.weights, static_cast<char*>(a.out), a.ld_out, a.dweights, a.cols);
     });
 }
 
+// Lanes of a row: two to four pieces each in short rows (8192 tokens of 100 bf16, six choices: 12 us
+// with 8 lanes, 35 with 64; 20000 of 1001: 78 with 32, 84 with 64), up to eight in long ones, and
+// whole workgroups where there are too few rows to fill the device with waves (one token of 16384,
+// eight choices: 5.3 us, a launch, against 12.3 with 64).
+template <int SIZE>
+c3_status gradient(const c3::SortArgs& a, hipStream_t stream) {
+    const int64_t pieces = pieces_of<SIZE>(a.cols), slots = a.T * a.top_k;
+    const bool large = (double)(2 * slots + a.T) * a.cols * SIZE > kLarge;
+    if (pieces <= 32) return launch_gradient<SIZE, 8, 4>(a, stream);
+    if (pieces <= 64) return launch_gradient<SIZE, 16, 4>(a, stream);
+    if (pieces <= 160) return launch_gradient<SIZE, 32, 4>(a, stream);
+    if (slots < 512 && pieces > 512) return launch_gradient<SIZE, 512, 4>(a, stream);
+    if (pieces <= 512) return large ? launch_gradient<SIZE, 64, 8>(a, stream) : launch_gradient<SIZE, 64, 4>(a, stream);
+    return large ? launch_gradient<SIZE, 128, 8>(a, stream) : launch_gradient<SIZE, 128, 4>(a, stream);
+}
+
 }  // namespace
 
 namespace c3 {
+
+// Rows by token where reading x again for every choice costs more than the launch that turns the
+// order round. Sorted by row and by token, 4096 bf16 and four choices: 256 tokens 5.3 and 8.0 us, 1024
+// tokens (67 MB read and written) 12.2 and 10.4; quantised 6.4 and 7.0, 14.4 and 9.4 (50 MB); 32768
+// tokens of eight choices 718 and 446.
+bool by_token(const SortArgs& a) {
+    const double size = a.dtype == C3_BF16 ? 2 : 4, values = (double)a.T * a.top_k * a.cols;
+    return a.scales ? values * (size + 1) > 20e6 : values * 2 * size > 48e6;
+}
 
 c3_status positions_enqueue(const SortArgs& a, hipStream_t stream) {
     const Plan g = plan_of(a);
@@ -228,7 +274,7 @@ c3_status combine_enqueue(const SortArgs& a, hipStream_t stream) {
 }
 
 c3_status combine_backward_enqueue(const SortArgs& a, hipStream_t stream) {
-    return a.dtype == C3_BF16 ? launch_gradient<2, 64>(a, stream) : launch_gradient<4, 64>(a, stream);
+    return a.dtype == C3_BF16 ? gradient<2>(a, stream) : gradient<4>(a, stream);
 }
 
 }  // namespace c3

@@ -232,6 +232,46 @@ def test_combine_backward_skips_bad_positions(c3gpu):
     assert (np.abs(dW.cpu().numpy() - dw) <= bound).all()
 
 
+@pytest.mark.parametrize("T,k,cols,dtype", [(2500, 8, 2049, 0), (9000, 6, 2400, 0), (4000, 6, 4301, 0), (5200, 3, 4100, 1), (9000, 2, 4096, 0)])
+def test_traffic_past_the_caches(c3gpu, T, k, cols, dtype):
+    """Sizes that take other kernels: sorted token by token with few and with many choices, fewer
+    choices in flight, rows by more lanes. Sums and gradients of some tokens, the sort of all."""
+    import torch
+
+    rng = np.random.default_rng(T + cols)
+    g = torch.Generator(device="cuda:0").manual_seed(T)
+    kind = torch.bfloat16 if dtype == 0 else torch.float32
+    order, offsets, n = routing(rng, T, 16, k, 0.05)
+    S = T * k
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda:0").to(kind)  # noqa: E731
+    x, pos = new(T, cols), torch.full((S,), -9, dtype=torch.int32, device="cuda:0")
+    y = torch.full((S, cols), CANARY, dtype=kind, device="cuda:0")
+    c3gpu.c3_dispatch(x, dtype, T, cols, cols, dev(order), dev(offsets), k, 16, y, cols, pos)
+    sync()
+    want = ref.positions(order, n, S)
+    np.testing.assert_array_equal(pos.cpu().numpy(), want)
+    assert torch.equal(y[:n], x[dev(order[:n] % T).long()]) and bool((y[n:] == CANARY).all())
+
+    y = new(S, cols)
+    w, dout = torch.randn(T, k, generator=g, device="cuda:0"), new(T, cols)
+    out, dy, dw = new(T, cols), torch.full((S, cols), CANARY, dtype=kind, device="cuda:0"), torch.empty(T, k, device="cuda:0")
+    c3gpu.c3_combine(y, dtype, T, k, cols, cols, pos, w, out, cols)
+    c3gpu.c3_combine_backward(dout, dtype, T, k, cols, cols, y, cols, pos, w, dy, cols, dw)
+    sync()
+    assert bool((dy[n:] == CANARY).all())
+    some = np.concatenate([np.arange(40), rng.integers(0, T, 200), np.arange(T - 40, T)])
+    at = want.reshape(k, T)[:, some]
+    rows = y[dev(np.maximum(at, 0).reshape(-1)).long()].float().cpu().numpy()
+    local = np.where(at >= 0, np.arange(at.size).reshape(at.shape), -1)  # the rows of these tokens alone
+    take = lambda t: t[dev(some).long()].float().cpu().numpy()  # noqa: E731
+    sums, bound = ref.combine(rows, local, take(w))
+    assert (np.abs(take(out) - sums) <= bound + ref.HALF[dtype] * (np.abs(sums) + bound)).all()
+    d, written, dws, bound = ref.combine_gradient(take(dout), rows, local, take(w))
+    got = dy[dev(np.maximum(at, 0).reshape(-1)).long()].float().cpu().numpy()
+    assert (np.abs(got - d) <= (ref.HALF[dtype] + 2.0 ** -24) * 1.01 * np.abs(d) + ref.TINY)[written].all()
+    assert (np.abs(take(dw) - dws) <= bound).all()
+
+
 def test_offsets_past_32_bits(c3gpu):
     """Rows of y whose byte and element offsets pass 2^32 and 2^31."""
     import torch
