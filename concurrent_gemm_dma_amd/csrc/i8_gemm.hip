@@ -106,7 +106,9 @@ __device__ __forceinline__ int count_tiles(const Args& g) {
 //
 // Bound by B's bytes where rows are few. Workgroups start at different stages of K (sums of integers
 // have no order): rows a power of two apart put one column into few memory channels, and all
-// workgroups in step would ask for that column at one time.
+// workgroups in step would ask for that column at one time. 1x28672x8192 38-40 us (6.0 TB/s), 47 in
+// step, 53 with fragments straight from memory, 64 contiguous bytes a row; 32 columns a workgroup
+// instead of 16 47; three and four stages a wave no faster.
 template <int BM, int NT, int W>
 __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
     constexpr int MT = BM / 16, BN = 16 * NT, TILE = BM * BN, STAGE = (BM + BN) * 128, LOADS = (BM + BN) / 8;
@@ -203,6 +205,17 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // those of one slice run, the wave reads the next slice's fragments; in the last and the next
 // stage's first it issues the loads that refill the buffer, one each GAP instructions.
 //
+// Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
+// an eighth of K further on (sums of integers have no order), so that not all ask the same memory
+// channels: 8192x28672x8192 in tiles of 128 1755 us against 1938, of 256 1471 against 1491; 1024 rows of
+// 8 experts x 8192x8192 108 against 132. Any further apart, the L2 is lost: 3025 and 1566.
+//
+// 8192x28672x8192 1.43-1.47 ms (2.6-2.7 POPS; hipBLASLt 1.90): matrix pipe busy 80% of the cycles at
+// 1.3-1.5 GHz under the power limit, at which matrix instructions alone, operands in registers and
+// random, reach 3.6 POPS (4.95 on zeros). A tile's start and end cost a CU 9-11 us of 256x256 (half of
+// it scaling and storing 64 K sums, half first loads), which short K shows. One workgroup a CU that fetched
+// the next tile's first stages before storing gained nothing: its stores then held up the loads.
+//
 // No load leaves its array: rows past the tile's are clamped to its last one, stages past the last
 // one load the last one again into a buffer nobody reads.
 template <int TM, int TN, int BUFS>
@@ -241,10 +254,9 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
     auto a_row = [&](int i) -> uint32_t { return (uint32_t)min(i, r.end - 1 - r.begin); };
     auto b_row = [&](int i) -> uint32_t { return (uint32_t)min(i, g.N - 1 - n0); };
 
-    // scales of the tile's rows and columns
-    float* scales = reinterpret_cast<float*>(smem + SCALES);
-    if (tid < BM) scales[tid] = g.sA[r.begin + a_row(tid)];
-    if (tid < BN) scales[BM + tid] = g.sB[b_base + b_row(tid)];
+    // scales of the tile's rows and columns, of use at the end only
+    const float scale_a = tid < BM ? g.sA[r.begin + a_row(tid)] : 0.f;
+    const float scale_b = tid < BN ? g.sB[b_base + b_row(tid)] : 0.f;
 
     i32x16_t acc[TM][TN];
 #pragma unroll
@@ -254,6 +266,7 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
 
     {
         const uint32_t row = (uint32_t)g.P, nk = row / 128;
+        const uint32_t first = (blockIdx.x & 7) * nk / 8;  // the XCD's first stage
         const i32x4_t rA = rsrc_of(g.A + (size_t)r.begin * row), rB = rsrc_of(g.B + b_base * row);
         // load i of wave w: rows 8 * (2 * T * w + i) + lane / 8, chunk lane % 8
         uint32_t va[2 * TM], vb[2 * TN];
@@ -266,7 +279,9 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
             vb[i] = b_row(8 * (2 * TN * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
         const uint32_t lds0 = (uint32_t)(uintptr_t)(C3_LDS char*)smem;
         auto load = [&](uint32_t stage, int buf, int i) {  // load i of a stage into a buffer
-            const uint32_t soff = min(stage, nk - 1) * 128u;
+            uint32_t k = min(stage, nk - 1) + first;
+            if (k >= nk) k -= nk;
+            const uint32_t soff = k * 128u;
             const uint32_t at = lds0 + (uint32_t)(buf * STAGE);
             if (i < 2 * TM) lds_load(rA, at + (uint32_t)((2 * TM * wave + i) * 1024), va[i < 2 * TM ? i : 0], soff);
             else lds_load(rB, at + (uint32_t)(BM * 128 + (2 * TN * wave + i - 2 * TM) * 1024), vb[i < 2 * TM ? 0 : i - 2 * TM], soff);
@@ -327,7 +342,6 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
             }
         };
 
-        C3_WAIT_VMCNT(0);  // the scales': what follows counts the stages' loads only
 #pragma unroll
         for (int st = 0; st < BUFS - 1; ++st)
 #pragma unroll
@@ -335,7 +349,6 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
 #pragma unroll
         for (int i = 0; i < LOADS / 2; ++i) load(BUFS - 1, BUFS - 1, i);
         C3_WAIT_VMCNT((BUFS - 2) * LOADS + LOADS / 2);
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // the scales' writes
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -349,19 +362,30 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
             if (p + b < nk) stage(p + b, b);
         C3_WAIT_VMCNT(0);  // loads past the end still write LDS
     }
+    float* scales = reinterpret_cast<float*>(smem + SCALES);
+    if (tid < BM) scales[tid] = scale_a;
+    if (tid < BN) scales[BM + tid] = scale_b;
     __syncthreads();
 
     // ---- C: through LDS (this wave's quarter of the stages), so that it leaves in whole 128-byte
     // lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each 32 x 32
     // block; a row's 16-byte chunks are permuted by its number against bank conflicts.
     char* out = smem + wave * (SCALES / 4);
-    const int m0w = r.begin + wm * 32 * TM, nw = n0 + wn * 32 * TN;
-    auto store = [&](auto f32_c, auto full_c) {
+    const int m0w = r.begin + wm * 32 * TM, nw = n0 + wn * 32 * TN, bytes = g.f32 ? 4 : 2;
+    // Whole 16-byte pieces in every column; aligned ones leave as stores into a buffer that ends behind
+    // the tile's last row, without a look at each.
+    enum { PARTS, PIECES, LINES };
+    const bool pieces = nw + 32 * TN <= g.N;
+    const bool lines = pieces && (((uintptr_t)g.C | (uint64_t)g.ldc * bytes) & 15) == 0 &&
+                       g.ldc * bytes * 32 * TM < (int64_t(1) << 31);
+    const int row_c = (int)(g.ldc * bytes), rows_c = min(32 * TM, r.end - m0w);
+    const auto rC = __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(g.C) + ((int64_t)m0w * g.ldc + nw) * bytes, 0,
+                                                      lines && rows_c > 0 ? (rows_c - 1) * row_c + 32 * TN * bytes : 0, 0x00020000);
+    auto store = [&](auto f32_c, auto mode_c) {
         constexpr bool F32 = decltype(f32_c)::value != 0;
-        constexpr bool FULL = decltype(full_c)::value != 0;  // whole 16-byte pieces only
+        constexpr int MODE = decltype(mode_c)::value;
         constexpr int size = F32 ? 4 : 2, row_bytes = 32 * TN * size, chunks = row_bytes / 16;
         constexpr int FIT = SCALES / 4 / (32 * row_bytes), PER = FIT < TM ? FIT : TM;  // 32-row blocks at once
-        const bool aligned = (((uintptr_t)g.C | (uint64_t)g.ldc * size) & 15) == 0;
 #pragma unroll
         for (int m0 = 0; m0 < TM; m0 += PER) {
 #pragma unroll
@@ -389,37 +413,39 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
             own_lds_fence();
 #pragma unroll
             for (int u = 0; u < PER * chunks / 2; ++u) {
-                const int i = u * 64 + lane, m = i / chunks, c = i % chunks, at = m0w + m0 * 32 + m;
-                const int n = nw + c * (16 / size);
-                if (at >= r.end || (!FULL && n >= g.N)) continue;
+                const int m = u * (64 / chunks) + lane / chunks, c = lane % chunks, at = m0w + m0 * 32 + m;
                 const i32x4_t v = *reinterpret_cast<const i32x4_t*>(out + m * row_bytes + (c ^ (m & (chunks - 1))) * 16);
+                if constexpr (MODE == LINES) {
+                    __builtin_amdgcn_raw_buffer_store_b128(v, rC, (m0 * 32 + m) * row_c + c * 16, 0, 0);
+                    continue;
+                }
+                const int n = nw + c * (16 / size);
+                if (at >= r.end || (MODE == PARTS && n >= g.N)) continue;
                 char* p = static_cast<char*>(g.C) + ((size_t)at * g.ldc + n) * size;
                 const int fit = (g.N - n) * size;
-                if (FULL || (fit >= 16 && aligned)) {
-                    *reinterpret_cast<i32x4_t*>(p) = v;
-                } else if (fit >= 16) {
-                    __builtin_memcpy(__builtin_assume_aligned(p, 2), &v, 16);
+                if (MODE == PIECES || fit >= 16) {
+                    __builtin_memcpy(__builtin_assume_aligned(p, size), &v, 16);
                 } else if constexpr (F32) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 3; ++e)
                         if (e * 4 < fit) reinterpret_cast<int*>(p)[e] = v[e];
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 7; ++e)
                         if (e * 2 < fit) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
                 }
             }
             own_lds_fence();
         }
     };
-    const int bytes = g.f32 ? 4 : 2;
-    const bool full = nw + 32 * TN <= g.N && (((uintptr_t)g.C | (uint64_t)g.ldc * bytes) & 15) == 0;
     if (g.f32) {
-        if (full) store(Int<1>{}, Int<1>{});
-        else store(Int<1>{}, Int<0>{});
+        if (lines) store(Int<1>{}, Int<LINES>{});
+        else if (pieces) store(Int<1>{}, Int<PIECES>{});
+        else store(Int<1>{}, Int<PARTS>{});
     } else {
-        if (full) store(Int<0>{}, Int<1>{});
-        else store(Int<0>{}, Int<0>{});
+        if (lines) store(Int<0>{}, Int<LINES>{});
+        else if (pieces) store(Int<0>{}, Int<PIECES>{});
+        else store(Int<0>{}, Int<PARTS>{});
     }
 }
 
@@ -497,14 +523,14 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
     // 128 rows: four stages in LDS where that costs no CU its second workgroup
     const bool alone = model.groups(128, 128) <= n_cu;
     Launch launch = alone ? launch_tile<2, 4> : launch_tile<2, 2>;
-    double least = model.tiles(128, 2 * n_cu, 4.97, 0.28, 1.18);
+    double least = model.tiles(128, 2 * n_cu, 4.84, 0.29, 1.11);
     auto consider = [&](double t, Launch l) {
         if (t < least) {
             least = t;
             launch = l;
         }
     };
-    consider(model.tiles(256, n_cu, 11.2, 1.02, 1.67), launch_tile<4, 2>);
+    consider(model.tiles(256, n_cu, 10.8, 1.05, 1.57), launch_tile<4, 2>);
     if (g.M <= 256 * (int64_t)model.used) {  // 5% off what the model says: it favours these
         auto rows = [&](int bm, int nt, int w) { return 1.05 * model.rows(bm, nt, w); };
         consider(rows(16, 1, 1), launch_rows<16, 1, 1>);
