@@ -122,9 +122,9 @@ __global__ __launch_bounds__(G > kThreads ? G : kThreads) void combine_gradient(
     constexpr int V = kValues<SIZE>, PER = G > kThreads ? 1 : kThreads / G;
     const int lane = threadIdx.x % G;
     const int64_t i = (int64_t)blockIdx.x * PER + threadIdx.x / G;
-    if (i >= pairs) return;  // whole groups, and whole workgroups where a group has several waves
-    const int64_t pair = first_pair + i, t = pair / g.top_k;
-    const int p = g.pos[(pair - t * g.top_k) * g.T + t];
+    const bool live = i < pairs;
+    const int64_t pair = first_pair + (live ? i : 0), t = pair / g.top_k;
+    const int p = live ? g.pos[(pair - t * g.top_k) * g.T + t] : -1;
     const bool here = p >= 0 && p < g.S;
     float sum = 0.f;
     if (here) {
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(G > kThreads ? G : kThreads) void combine_gradient(
             for (int v = 0; v < G / 64; ++v) sum += part[threadIdx.x / 64 + v];
         }
     }
-    if (lane == 0) dweights[pair] = here ? sum : 0.f;
+    if (lane == 0 && live) dweights[pair] = here ? sum : 0.f;
 }
 
 Plan plan_of(const c3::SortArgs& a) {
