@@ -200,10 +200,11 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // Tile kernel
 // ------------------------------------------------------------------------------------------------
 // 4 waves (2 x 2), each 32*TM x 32*TN of C from v_mfma_i32_32x32x32_i8 (lane l: row l % 32, 16 of
-// the slice's 32 columns). K goes in stages of 128 columns: a whole line of a row. BUFS stages are
+// the slice's 32 columns): 256x256 for full devices, 128x128, 128x64 and 64x64 to have a tile for every
+// CU. K goes in stages of 128 columns: a whole line of a row. BUFS stages are
 // in LDS. A stage is four slices of TM*TN matrix instructions, one barrier before the last. While
 // those of one slice run, the wave reads the next slice's fragments; in the last and the next
-// stage's first it issues the loads that refill the buffer, one each GAP instructions.
+// stage's first it issues the loads that refill the buffer, spread over the instructions.
 //
 // Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
 // an eighth of K further on (sums of integers have no order), so that not all ask the same memory
@@ -224,7 +225,6 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
     constexpr int STAGE = ROWS * 128, SCALES = BUFS * STAGE;
     constexpr int NM = TM * TN, NF = TM + TN;  // matrix instructions of a slice, fragments
     constexpr int LOADS = 2 * (TM + TN);       // loads of a wave and stage
-    constexpr int GAP = 2 * NM / LOADS;        // matrix instructions between two of them
     __shared__ __attribute__((aligned(1024))) char smem[SCALES + ROWS * 4];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -309,24 +309,37 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
         // One stage p in buffer `buf`. Its last slice and the next stage's first issue the loads of
         // stage p + BUFS into `buf`, whose last reader finished before the barrier. When stage p + 1
         // has to have landed, the loads of stages p + 2 .. p + BUFS - 1 may still be in flight.
+        // One fragment an instruction as long as there are some, or two.
+        auto reads = [](int i, auto f) {
+            constexpr int EACH = (NF + NM - 1) / NM;
+#pragma unroll
+            for (int l = i * EACH; l < i * EACH + EACH && l < NF; ++l) f(l);
+        };
+        // Instruction i of a slice's NM has its share of `n` reads or loads next to it.
+        auto share = [](int i, int n, auto f) {
+#pragma unroll
+            for (int l = 0; l < n; ++l)
+                if (l * NM / n == i) f(l);
+        };
         auto stage = [&](uint32_t p, int buf) {
+            const int last = (buf + BUFS - 1) & (BUFS - 1), next = (buf + 1) & (BUFS - 1);
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
                 mma(i, Int<0>{});
-                if (i < NF) read_frag(buf, 0, 1, i);
-                if (i % GAP == GAP - 1) load(p + BUFS - 1, (buf + BUFS - 1) & (BUFS - 1), LOADS / 2 + i / GAP);
+                reads(i, [&](int f) { read_frag(buf, 0, 1, f); });
+                share(i, LOADS / 2, [&](int l) { load(p + BUFS - 1, last, LOADS / 2 + l); });
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
                 mma(i, Int<1>{});
-                if (i < NF) read_frag(buf, 1, 0, i);
+                reads(i, [&](int f) { read_frag(buf, 1, 0, f); });
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
                 mma(i, Int<0>{});
-                if (i < NF) read_frag(buf, 1, 1, i);
+                reads(i, [&](int f) { read_frag(buf, 1, 1, f); });
                 __builtin_amdgcn_sched_barrier(0);
             }
             C3_WAIT_VMCNT((BUFS - 2) * LOADS);
@@ -336,8 +349,8 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
 #pragma unroll
             for (int i = 0; i < NM; ++i) {
                 mma(i, Int<1>{});
-                if (i < NF) read_frag((buf + 1) & (BUFS - 1), 0, 0, i);
-                if (i % GAP == 0) load(p + BUFS, buf, i / GAP);
+                reads(i, [&](int f) { read_frag(next, 0, 0, f); });
+                share(i, LOADS / 2, [&](int l) { load(p + BUFS, buf, l); });
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -385,7 +398,7 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
         constexpr bool F32 = decltype(f32_c)::value != 0;
         constexpr int MODE = decltype(mode_c)::value;
         constexpr int size = F32 ? 4 : 2, row_bytes = 32 * TN * size, chunks = row_bytes / 16;
-        constexpr int FIT = SCALES / 4 / (32 * row_bytes), PER = FIT < TM ? FIT : TM;  // 32-row blocks at once
+        constexpr int FIT = SCALES / 4 / (32 * row_bytes), PER = FIT >= TM ? TM : FIT >= TM / 2 ? TM / 2 : 1;  // 32-row blocks at once
 #pragma unroll
         for (int m0 = 0; m0 < TM; m0 += PER) {
 #pragma unroll
@@ -465,19 +478,23 @@ bool launch_rows(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
 }
 
 // false: as above.
-template <int T, int BUFS>
+template <int TM, int TN, int BUFS>
 bool launch_tile(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
-    constexpr int BM = 64 * T;
-    const int64_t groups = most_tiles(g, BM) * ((g.N + BM - 1) / BM);
+    constexpr int BM = 64 * TM, BN = 64 * TN;
+    const int64_t groups = most_tiles(g, BM) * ((g.N + BN - 1) / BN);
     if (groups * 256 >= (int64_t(1) << 32)) return false;
-    hipLaunchKernelGGL((i8_gemm_tile<T, T, BUFS>), dim3((unsigned)groups), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((i8_gemm_tile<TM, TN, BUFS>), dim3((unsigned)groups), dim3(256), 0, stream, a);
     return true;
 }
 typedef bool (*Launch)(const c3::I8Gemm&, const Args&, hipStream_t);
 
-// What a launch would take, in us: a model of where the time goes, its constants fitted to 340 shapes
-// of 1 to 20000 rows, one matrix or up to 64 experts' (each kernel's times to within 11%, rms; what
-// it chooses is 3.4% slower than the fastest of all on average).
+// What a launch would take, in us: a model of where the time goes, its constants fitted to 400 shapes
+// of 1 to 20000 rows, one matrix or up to 64 experts' (each kernel's times to within 7-13%, rms; what
+// it chooses is 2.5% slower than the fastest of all on average). Left out, the kernel of 16 rows would
+// cost 3% on average and up to 4x, tiles of 128x128 4%, of 64x64 2%, the others 0.5% each and up to 35%.
+// Some of the shapes (us): 198x3055x2199 rows 10.3, 64x64 6.3, 128x64 8.3, 128x128 11.3; 300x4096x4096
+// 15.1, 11.3 and 14.6 in tiles; 777x4999x4000 34, 34 and 29, 256x256 47; 4096x4096x4096 128x128 72,
+// 256x256 62; 1388x141x5565 64x64 10.5, 128x128 19.1.
 struct Model {
     const c3::I8Gemm& g;
     double n_cu, nk, used, memory;  // stages; experts with rows; the operands' and C's bytes at 6.2 TB/s
@@ -497,15 +514,16 @@ struct Model {
         const int bn = 16 * nt;
         const double per_cu = std::ceil(groups(bm, bn) / n_cu), all = per_cu * n_cu;
         const double lines = bn + std::max(2.0, std::min<double>(bm, g.M / used));
-        const double work = all * (lines * nk * 128 / 23.4e6 + bm * bn * nk * 256 / 4.06e9 + bm * bn * 2.49e-6);
+        const double work = all * (lines * nk * 128 / 20.0e6 + bm * bn * nk * 256 / 9.0e9 + bm * bn * 1.29e-6);
         const double rounds = std::max(1.0, per_cu / std::min(163840 / (2 * w * (bm + bn) * 128), 32 / w));
-        const double chain = rounds * (2.37 + nk / w * 0.03 * (bm + bn) / 8);
-        return 2.1 + std::sqrt(memory * memory + work * work + chain * chain);
+        const double chain = rounds * (2.26 + nk / w * 0.0232 * (bm + bn) / 8);
+        // 1.5% less for each doubling of waves, which keep memory busier where it bounds the time
+        return (2.4 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * std::log2(w));
     }
     // Rounds of `slots` tiles, each a fixed part and, per stage, between `low` and `high` with the share
     // of the device that it fills.
-    double tiles(int bm, double slots, double fixed, double low, double high) const {
-        const double n = groups(bm, bm), whole = std::floor(n / slots), rest = n - whole * slots;
+    double tiles(int bm, int bn, double slots, double fixed, double low, double high) const {
+        const double n = groups(bm, bn), whole = std::floor(n / slots), rest = n - whole * slots;
         const double t = whole * (fixed + high * nk) + (rest > 0 ? fixed + (low + (high - low) * rest / slots) * nk : 0);
         return std::sqrt(memory * memory + t * t);
     }
@@ -520,32 +538,29 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
                     (int)(g.dtype == C3_F32)};
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
     const Model model(g, a.P, n_cu);
-    // 128 rows: four stages in LDS where that costs no CU its second workgroup
-    const bool alone = model.groups(128, 128) <= n_cu;
-    Launch launch = alone ? launch_tile<2, 4> : launch_tile<2, 2>;
-    double least = model.tiles(128, 2 * n_cu, 4.84, 0.29, 1.11);
+    // 128x128: four stages in LDS where that costs no CU its second workgroup
+    Launch launch = model.groups(128, 128) <= n_cu ? launch_tile<2, 2, 4> : launch_tile<2, 2, 2>;
+    double least = model.tiles(128, 128, 2 * n_cu, 4.97, 0.272, 1.07);
     auto consider = [&](double t, Launch l) {
         if (t < least) {
             least = t;
             launch = l;
         }
     };
-    consider(model.tiles(256, n_cu, 10.8, 1.05, 1.57), launch_tile<4, 2>);
-    if (g.M <= 256 * (int64_t)model.used) {  // 5% off what the model says: it favours these
-        auto rows = [&](int bm, int nt, int w) { return 1.05 * model.rows(bm, nt, w); };
-        consider(rows(16, 1, 1), launch_rows<16, 1, 1>);
-        consider(rows(16, 1, 2), launch_rows<16, 1, 2>);
-        consider(rows(16, 1, 4), launch_rows<16, 1, 4>);
-        consider(rows(16, 1, 8), launch_rows<16, 1, 8>);
-        consider(rows(32, 2, 1), launch_rows<32, 2, 1>);
-        consider(rows(32, 2, 2), launch_rows<32, 2, 2>);
-        consider(rows(32, 2, 4), launch_rows<32, 2, 4>);
-        consider(rows(32, 2, 8), launch_rows<32, 2, 8>);
-        consider(rows(64, 4, 1), launch_rows<64, 4, 1>);
-        consider(rows(64, 4, 2), launch_rows<64, 4, 2>);
-        consider(rows(64, 4, 4), launch_rows<64, 4, 4>);
+    consider(model.tiles(256, 256, n_cu, 10.8, 0.967, 1.58), launch_tile<4, 4, 2>);
+    consider(model.tiles(128, 64, n_cu, 4.12, 0.231, 0.275), launch_tile<2, 1, 4>);
+    consider(model.tiles(64, 64, 2 * n_cu, 4.38, 0.114, 0.348), launch_tile<1, 1, 4>);
+    if (g.M <= 256 * (int64_t)model.used) {
+        consider(model.rows(16, 1, 1), launch_rows<16, 1, 1>);
+        consider(model.rows(16, 1, 2), launch_rows<16, 1, 2>);
+        consider(model.rows(16, 1, 4), launch_rows<16, 1, 4>);
+        consider(model.rows(16, 1, 8), launch_rows<16, 1, 8>);
+        consider(model.rows(32, 2, 1), launch_rows<32, 2, 1>);
+        consider(model.rows(32, 2, 2), launch_rows<32, 2, 2>);
+        consider(model.rows(32, 2, 4), launch_rows<32, 2, 4>);
+        consider(model.rows(32, 2, 8), launch_rows<32, 2, 8>);
     }
-    if (!launch(g, a, stream) && !launch_tile<4, 2>(g, a, stream))
+    if (!launch(g, a, stream) && !launch_tile<4, 4, 2>(g, a, stream))
         return fail(C3_E_INVALID, "int8 product: too many tiles");
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;
