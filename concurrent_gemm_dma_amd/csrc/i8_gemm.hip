@@ -518,7 +518,7 @@ struct Model {
         const double rounds = std::max(1.0, per_cu / std::min(163840 / (2 * w * (bm + bn) * 128), 32 / w));
         const double chain = rounds * (2.26 + nk / w * 0.0232 * (bm + bn) / 8);
         // 1.5% less for each doubling of waves, which keep memory busier where it bounds the time
-        return (2.4 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * std::log2(w));
+        return (2.4 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * __builtin_ctz(w));
     }
     // Rounds of `slots` tiles, each a fixed part and, per stage, between `low` and `high` with the share
     // of the device that it fills.
