@@ -201,17 +201,17 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // ------------------------------------------------------------------------------------------------
 // 4 waves (2 x 2), each 32*TM x 32*TN of C from v_mfma_i32_32x32x32_i8 (lane l: row l % 32, 16 of
 // the slice's 32 columns): 256x256 for full devices, 128x128, 128x64 and 64x64 to have a tile for every
-// CU. K goes in stages of 128 columns: a whole line of a row. BUFS stages are
-// in LDS. A stage is four slices of TM*TN matrix instructions, one barrier before the last. While
-// those of one slice run, the wave reads the next slice's fragments; in the last and the next
-// stage's first it issues the loads that refill the buffer, spread over the instructions.
+// CU. K goes in stages of 128 columns: a whole line of a row. BUFS stages are in LDS. A stage is four
+// slices of TM*TN matrix instructions, one barrier before the last. While those of one slice run, the
+// wave reads the next slice's fragments; in the last and the next stage's first it issues the loads
+// that refill the buffer, spread over the instructions (all of them in the last slice 3-5% slower).
 //
 // Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
 // an eighth of K further on (sums of integers have no order), so that not all ask the same memory
 // channels: 8192x28672x8192 in tiles of 128 1755 us against 1938, of 256 1471 against 1491; 1024 rows of
 // 8 experts x 8192x8192 108 against 132. Any further apart, the L2 is lost: 3025 and 1566.
 //
-// 8192x28672x8192 1.43-1.47 ms (2.6-2.7 POPS; hipBLASLt 1.90): matrix pipe busy 80% of the cycles at
+// 8192x28672x8192 1.35-1.47 ms (2.6-2.8 POPS; hipBLASLt 1.90): matrix pipe busy 80% of the cycles at
 // 1.3-1.5 GHz under the power limit, at which matrix instructions alone, operands in registers and
 // random, reach 3.6 POPS (4.95 on zeros). A tile's start and end cost a CU 9-11 us of 256x256 (half of
 // it scaling and storing 64 K sums, half first loads), which short K shows. One workgroup a CU that fetched
@@ -306,9 +306,6 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
             const int mi = i / TN, ni = (mi & 1) ? TN - 1 - i % TN : i % TN;
             acc[mi][ni] = __builtin_amdgcn_mfma_i32_32x32x32_i8(frag[J][TM + ni], frag[J][mi], acc[mi][ni], 0, 0, 0);
         };
-        // One stage p in buffer `buf`. Its last slice and the next stage's first issue the loads of
-        // stage p + BUFS into `buf`, whose last reader finished before the barrier. When stage p + 1
-        // has to have landed, the loads of stages p + 2 .. p + BUFS - 1 may still be in flight.
         // One fragment an instruction as long as there are some, or two.
         auto reads = [](int i, auto f) {
             constexpr int EACH = (NF + NM - 1) / NM;
@@ -321,6 +318,9 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
             for (int l = 0; l < n; ++l)
                 if (l * NM / n == i) f(l);
         };
+        // One stage p in buffer `buf`. Its last slice and the next stage's first issue the loads of
+        // stage p + BUFS into `buf`, whose last reader finished before the barrier. When stage p + 1
+        // has to have landed, the loads of stages p + 2 .. p + BUFS - 1 may still be in flight.
         auto stage = [&](uint32_t p, int buf) {
             const int last = (buf + BUFS - 1) & (BUFS - 1), next = (buf + 1) & (BUFS - 1);
 #pragma unroll

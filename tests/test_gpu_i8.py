@@ -266,6 +266,41 @@ def test_experts_loads(c3gpu, sizes):
     experts(c3gpu, rng, np.concatenate([[0], np.cumsum(sizes)]), 500, 4, 264, 256, 0)
 
 
+# Shapes for every kernel that the products choose from, with stages of K that are and that are not a
+# multiple of those in flight: rows of 16 and of 32 by one to eight waves, tiles of 64x64, 128x64,
+# 128x128 (a CU to itself or not) and 256x256; with experts, up to 64 of them and more.
+EVERY = [(260, 11923, 670), (261, 10960, 540), (8572, 206, 668), (8379, 198, 545), (6813, 65, 684), (5577, 66, 569),
+         (919, 9425, 669), (7812, 1171, 545), (259, 30, 670), (258, 30, 545), (1, 8263, 674), (1, 8222, 542), (1, 30, 669),
+         (1, 30, 541), (18, 8413, 681), (18, 8248, 550), (130, 902, 672), (210, 578, 545)]
+EVERY_EXPERTS = [(3167, 100, 261, 676), (3180, 100, 259, 548), (7214, 100, 135, 677), (7332, 100, 136, 567),
+                 (3813, 100, 65, 683), (4615, 70, 65, 546), (8800, 24, 946, 669), (4345, 24, 1943, 568),
+                 (8941, 70, 656, 2680), (1291, 5, 32, 717), (1327, 5, 30, 566), (101, 100, 494, 668), (83, 70, 648, 540),
+                 (105, 100, 195, 691), (113, 100, 197, 548), (2216, 100, 33, 673), (2391, 100, 33, 552),
+                 (1, 5, 30, 668), (1, 5, 30, 547), (1638, 100, 420, 668), (1914, 100, 386, 542), (805, 70, 484, 677),
+                 (904, 70, 461, 542), (2384, 100, 66, 726), (1382, 70, 115, 540), (2626, 24, 35, 691),
+                 (2508, 24, 36, 545)]
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("M,N,K", EVERY)
+def test_every_kernel(c3gpu, M, N, K, dtype):
+    rng = np.random.default_rng(M + N + K)
+    (A, sA), (B, sB) = operand(rng, M, K), operand(rng, N, K)
+    C = Rows(M, N, dtype, N + N % 3, M % 2)
+    c3gpu.c3_i8_gemm(dev(A), dev(sA), dev(B), dev(sB), C.ptr(), dtype, M, N, K, C.ld)
+    sync()
+    C.intact()
+    np.testing.assert_array_equal(C.numpy(), ref.rounded(ref.product(A, sA, B, sB), dtype))
+
+
+@pytest.mark.parametrize("i", range(len(EVERY_EXPERTS)))
+def test_every_kernel_of_experts(c3gpu, i):
+    rows, E, N, K = EVERY_EXPERTS[i]
+    rng = np.random.default_rng(rows + E)
+    cut = np.sort(rng.integers(0, rows + 1, E + 1))
+    experts(c3gpu, rng, cut, rows, E, N, K, i % 2, N + N % 3, i % 3)
+
+
 def test_experts_every_border_of_few_rows(c3gpu):
     rng = np.random.default_rng(4)
     for rows in (1, 15, 16, 17, 31, 32, 33, 47, 64, 65):
@@ -308,14 +343,15 @@ def test_unaligned_scales_and_strided_output(c3gpu):
             np.testing.assert_array_equal(C.numpy(), want)
 
 
-def test_in_a_captured_graph_and_on_streams(c3gpu):
+@pytest.mark.parametrize("T", [24, 8000])
+def test_in_a_captured_graph_and_on_streams(c3gpu, T):
     """Sort, product of every expert and combination in one graph, replayed on new inputs between
     eager calls; the same bits."""
     import torch
 
     c3 = c3gpu
     rng = np.random.default_rng(21)
-    T, E, k, D, F = 24, 8, 2, 520, 264
+    E, k, D, F = 8, 2, 520, 264
     S = T * k
     new = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device="cuda:0")  # noqa: E731
     x, w, order, offsets = new(T, D), new(T, k, t=torch.float32), new(S, t=torch.int32), new(E + 1, t=torch.int32)

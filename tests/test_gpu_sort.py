@@ -301,7 +301,7 @@ def test_offsets_past_32_bits(c3gpu):
     assert (np.abs(dw.cpu().numpy() - want[:, None]) <= 1.01 * (cols + 16) * 2.0 ** -24 * want[:, None]).all()
 
 
-@pytest.mark.parametrize("T,E,k,cols", [(4, 8, 2, 96), (2000, 16, 4, 512)])
+@pytest.mark.parametrize("T,E,k,cols", [(4, 8, 2, 96), (2000, 16, 4, 512), (4000, 16, 8, 1024)])
 def test_in_a_captured_graph(c3gpu, T, E, k, cols):
     """Dispatch, combine and its gradient captured once, replayed on new inputs with eager work of
     the same buffers' shapes between the replays; the same bits as eager calls."""
@@ -347,6 +347,74 @@ def test_in_a_captured_graph(c3gpu, T, E, k, cols):
         sync()
         for name in held:
             assert torch.equal(held[name], eager[name]), name
+
+
+def test_an_expert_named_twice(c3gpu):
+    """Both choices of a token may have one expert: two slots, two rows, two weights."""
+    import torch
+
+    rng = np.random.default_rng(13)
+    T, E, k, cols = 200, 4, 3, 70
+    idx = rng.integers(0, E, (T, k)).astype(np.int32)
+    order, offsets = ref.plan(idx, E)
+    x, w = Rows(T, cols, 1, values=values(rng, (T, cols), 1)), rng.random((T, k)).astype(np.float32)
+    y, pos = Rows(T * k, cols, 1), torch.empty(T * k, dtype=torch.int32, device="cuda:0")
+    out = Rows(T, cols, 1)
+    c3gpu.c3_dispatch(x.ptr(), 1, T, cols, cols, dev(order), dev(offsets), k, E, y.ptr(), cols, pos)
+    c3gpu.c3_combine(y.ptr(), 1, T, k, cols, cols, pos, dev(w), out.ptr(), cols)
+    sync()
+    np.testing.assert_array_equal(y.numpy(), ref.sort_rows(x.numpy(), order, T * k))
+    want, bound = ref.combine(y.numpy(), ref.positions(order, T * k, T * k).reshape(k, T), w)
+    assert (np.abs(out.numpy() - want) <= bound + ref.HALF[1] * (np.abs(want) + bound)).all()
+
+
+def test_calls_from_several_host_threads(c3gpu):
+    """Threads with a stream and buffers each, all operators in turn; every one gets its own answer."""
+    import threading
+
+    import torch
+
+    c3 = c3gpu
+    T, E, k, cols, n = 300, 8, 2, 264, 4
+    rng = np.random.default_rng(14)
+    jobs, bad = [], []
+    for _ in range(n):
+        order, offsets, m = routing(rng, T, E, k, 0.1)
+        jobs.append({"x": dev(values(rng, (T, cols), 1)), "order": dev(order), "offsets": dev(offsets), "n": m,
+                     "host": order, "y": torch.zeros(T * k, cols, device="cuda:0"), "stream": torch.cuda.Stream(),
+                     "pos": torch.zeros(T * k, dtype=torch.int32, device="cuda:0"), "out": torch.zeros(T, cols, device="cuda:0"),
+                     "codes": torch.zeros(T * k, ref.padded(cols), dtype=torch.int8, device="cuda:0"),
+                     "scales": torch.zeros(T * k, device="cuda:0"), "C": torch.zeros(T * k, T * k, device="cuda:0")})
+    sync()
+
+    def work(j):
+        try:
+            for _ in range(20):
+                c3.c3_dispatch(j["x"], 1, T, cols, cols, j["order"], j["offsets"], k, E, j["y"], cols, j["pos"], j["stream"])
+                c3.c3_combine(j["y"], 1, T, k, cols, cols, j["pos"], None, j["out"], cols, j["stream"])
+                c3.c3_i8_dispatch(j["x"], 1, T, cols, cols, j["order"], j["offsets"], k, E, j["codes"], j["scales"],
+                                  j["pos"], j["stream"])
+                c3.c3_i8_gemm(j["codes"], j["scales"], j["codes"], j["scales"], j["C"], 1, T * k, T * k, cols, T * k,
+                              j["stream"])
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    sync()
+    assert not bad, bad
+    for j in jobs:
+        x, order, m = j["x"].cpu().numpy(), j["host"], j["n"]
+        np.testing.assert_array_equal(j["y"].cpu().numpy()[:m], ref.sort_rows(x, order, m))
+        pos = ref.positions(order, m, T * k).reshape(k, T)
+        want, bound = ref.combine(j["y"].cpu().numpy(), pos, None)
+        assert (np.abs(j["out"].cpu().numpy() - want) <= bound + ref.HALF[1] * (np.abs(want) + bound)).all()
+        A, s = ref.quantize(x)
+        A, s = A[order[:m] % T], s[order[:m] % T]
+        np.testing.assert_array_equal(j["C"].cpu().numpy()[:m, :m], ref.product(A, s, A, s))
 
 
 def test_two_streams_and_repeats_give_the_same_bits(c3gpu):
