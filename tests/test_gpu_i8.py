@@ -40,7 +40,7 @@ def quantise(c3, x, dtype, ld=None, shift=0, stream=None):
 @pytest.mark.parametrize("rows,cols,more,shift", [
     (1, 1, 0, 0), (1, 128, 0, 0), (3, 127, 0, 1), (2, 129, 3, 0), (5, 1000, 0, 3), (130, 136, 0, 0), (9, 2048, 0, 0),
     (7, 2049, 1, 0), (1, 16384, 0, 0), (40, 16384, 0, 0), (3, 16385, 0, 5), (2, 70001, 0, 0), (1000, 520, 8, 0),
-    (5000, 72, 0, 0), (700, 4096, 0, 0), (1, 131072, 0, 0)])
+    (5000, 72, 0, 0), (700, 4096, 0, 0), (1, 131072, 0, 0), (50, 400, 0, 0)])
 def test_quantise(c3gpu, rows, cols, more, shift, dtype):
     x = wide(np.random.default_rng(rows * 7919 + cols), rows, cols, dtype)
     codes, scales = quantise(c3gpu, x, dtype, cols + more, shift)
@@ -94,7 +94,9 @@ def test_quantise_values_next_to_borders(c3gpu):
 @pytest.mark.parametrize("T,E,k,cols,more,shift,masked", [
     (1, 4, 4, 4096, 0, 0, 0.0), (3, 8, 2, 7, 1, 3, 0.0), (8, 32, 4, 16385, 0, 0, 0.0), (17, 5, 3, 129, 0, 1, 0.3),
     (700, 16, 8, 520, 0, 0, 0.1), (6000, 64, 7, 65, 3, 5, 0.05), (1030, 24, 3, 5000, 0, 0, 0.1), (40, 8, 2, 640, 0, 0, 1.0),
-    (900, 16, 8, 2048, 0, 0, 0.0), (300, 16, 8, 17000, 0, 0, 0.1)])
+    (900, 16, 8, 2048, 0, 0, 0.0), (300, 16, 8, 17000, 0, 0, 0.1), (20, 8, 2, 1500, 0, 0, 0.1), (20, 8, 2, 6000, 0, 0, 0.1),
+    (20, 8, 2, 12001, 0, 0, 0.1), (10000, 16, 7, 100, 0, 0, 0.1), (5100, 16, 7, 200, 1, 0, 0.1), (2600, 16, 7, 400, 0, 0, 0.1),
+    (600, 16, 3, 4000, 0, 1, 0.1), (150, 16, 3, 16000, 0, 0, 0.1)])
 def test_sorted_quantise(c3gpu, T, E, k, cols, more, shift, masked, dtype):
     import torch
 

@@ -68,7 +68,8 @@ def values(rng, shape, dtype):
 CASES = [(1, 1, 1, 1, 0, 0, 0.0), (1, 4, 4, 4096, 0, 0, 0.0), (1, 8, 3, 16385, 7, 1, 0.0), (3, 8, 2, 7, 1, 3, 0.0),
          (8, 32, 4, 4096, 0, 0, 0.0), (17, 5, 3, 129, 0, 1, 0.3), (33, 6, 2, 1000, 24, 0, 0.1),
          (5, 64, 64, 40, 0, 0, 0.2), (700, 16, 8, 520, 0, 0, 0.1), (6000, 64, 7, 65, 3, 5, 0.05),
-         (9000, 256, 8, 8, 0, 0, 0.0), (4099, 24, 3, 2049, 0, 0, 0.1), (40, 8, 2, 640, 0, 0, 1.0)]
+         (9000, 256, 8, 8, 0, 0, 0.0), (4099, 24, 3, 2049, 0, 0, 0.1), (40, 8, 2, 640, 0, 0, 1.0),
+         (300, 8, 2, 5001, 0, 0, 0.1)]
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
@@ -232,7 +233,8 @@ def test_combine_backward_skips_bad_positions(c3gpu):
     assert (np.abs(dW.cpu().numpy() - dw) <= bound).all()
 
 
-@pytest.mark.parametrize("T,k,cols,dtype", [(2500, 8, 2049, 0), (9000, 6, 2400, 0), (4000, 6, 4301, 0), (5200, 3, 4100, 1), (9000, 2, 4096, 0)])
+@pytest.mark.parametrize("T,k,cols,dtype", [(2500, 8, 2049, 0), (9000, 6, 2400, 0), (4000, 6, 4301, 0), (5200, 3, 4100, 1), (9000, 2, 4096, 0),
+                                              (6000, 5, 2000, 1)])
 def test_traffic_past_the_caches(c3gpu, T, k, cols, dtype):
     """Sizes that take other kernels: sorted token by token with few and with many choices, fewer
     choices in flight, rows by more lanes. Sums and gradients of some tokens, the sort of all."""
