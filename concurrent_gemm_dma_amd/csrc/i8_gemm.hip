@@ -199,12 +199,16 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // ------------------------------------------------------------------------------------------------
 // Tile kernel
 // ------------------------------------------------------------------------------------------------
-// 4 waves (2 x 2), each 32*TM x 32*TN of C from v_mfma_i32_32x32x32_i8 (lane l: row l % 32, 16 of
-// the slice's 32 columns): 256x256 for full devices, 128x128, 128x64 and 64x64 to have a tile for every
-// CU. K goes in stages of 128 columns: a whole line of a row. BUFS stages are in LDS. A stage is four
-// slices of TM*TN matrix instructions, one barrier before the last. While those of one slice run, the
-// wave reads the next slice's fragments; in the last and the next stage's first it issues the loads
-// that refill the buffer, spread over the instructions (all of them in the last slice 3-5% slower).
+// 2 x WN waves, each 32*TM x 32*TN of C from v_mfma_i32_32x32x32_i8 (lane l: row l % 32, 16 of the
+// slice's 32 columns): 256x256 for full devices, 128x128, 128x64 and 64x64 to have a tile for every CU.
+// K goes in stages of 128 columns: a whole line of a row. BUFS stages are in LDS. A stage is four slices
+// of TM*TN matrix instructions, one barrier before the last. While those of one slice run, the wave
+// reads the next slice's fragments; in the last and the next stage's first it issues the loads that
+// refill the buffer, spread over the instructions (all of them in the last slice 3-5% slower).
+//
+// 256x256 comes with 4 waves, which read least from LDS and take 2% less on long K, and with 8, of which
+// one scales and stores while another still multiplies: 8192x28672x512 239 us against 270,
+// 16384 rows of 8 experts x 14336x4096 890 against 872. 128x128 with 8: 73 us against 76 on 4096x4096x4096.
 //
 // Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
 // an eighth of K further on (sums of integers have no order), so that not all ask the same memory
@@ -219,17 +223,17 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 //
 // No load leaves its array: rows past the tile's are clamped to its last one, stages past the last
 // one load the last one again into a buffer nobody reads.
-template <int TM, int TN, int BUFS>
-__global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gemm_tile(const Args g) {
-    constexpr int BM = 64 * TM, BN = 64 * TN, ROWS = BM + BN;
+template <int TM, int TN, int BUFS, int WN>
+__global__ __launch_bounds__(128 * WN, TM * TN == 16 || BUFS > 2 || WN > 2 ? 1 : 2) void i8_gemm_tile(const Args g) {
+    constexpr int BM = 64 * TM, BN = 32 * WN * TN, ROWS = BM + BN, WAVES = 2 * WN;
     constexpr int STAGE = ROWS * 128, SCALES = BUFS * STAGE;
     constexpr int NM = TM * TN, NF = TM + TN;  // matrix instructions of a slice, fragments
-    constexpr int LOADS = 2 * (TM + TN);       // loads of a wave and stage
+    constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES, LOADS = LA + LB;  // loads of a wave and stage
     __shared__ __attribute__((aligned(1024))) char smem[SCALES + ROWS * 4];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
+    const int wm = wave / WN, wn = wave % WN;
     const int tiles_n = (g.N + BN - 1) / BN;
     int tm, tn;
     Rows r;
@@ -268,23 +272,23 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
         const uint32_t row = (uint32_t)g.P, nk = row / 128;
         const uint32_t first = (blockIdx.x & 7) * nk / 8;  // the XCD's first stage
         const i32x4_t rA = rsrc_of(g.A + (size_t)r.begin * row), rB = rsrc_of(g.B + b_base * row);
-        // load i of wave w: rows 8 * (2 * T * w + i) + lane / 8, chunk lane % 8
-        uint32_t va[2 * TM], vb[2 * TN];
+        // load i of wave w: rows 8 * (LA * w + i) + lane / 8 of A, chunk lane % 8; the same of B
+        uint32_t va[LA], vb[LB];
         const int q = lane >> 3;
 #pragma unroll
-        for (int i = 0; i < 2 * TM; ++i)
-            va[i] = a_row(8 * (2 * TM * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
+        for (int i = 0; i < LA; ++i)
+            va[i] = a_row(8 * (LA * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * (LA * wave + i) + q)) * 16u;
 #pragma unroll
-        for (int i = 0; i < 2 * TN; ++i)
-            vb[i] = b_row(8 * (2 * TN * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * i + q)) * 16u;
+        for (int i = 0; i < LB; ++i)
+            vb[i] = b_row(8 * (LB * wave + i) + q) * row + (uint32_t)((lane & 7) ^ swizzle(8 * (LB * wave + i) + q)) * 16u;
         const uint32_t lds0 = (uint32_t)(uintptr_t)(C3_LDS char*)smem;
         auto load = [&](uint32_t stage, int buf, int i) {  // load i of a stage into a buffer
             uint32_t k = min(stage, nk - 1) + first;
             if (k >= nk) k -= nk;
             const uint32_t soff = k * 128u;
             const uint32_t at = lds0 + (uint32_t)(buf * STAGE);
-            if (i < 2 * TM) lds_load(rA, at + (uint32_t)((2 * TM * wave + i) * 1024), va[i < 2 * TM ? i : 0], soff);
-            else lds_load(rB, at + (uint32_t)(BM * 128 + (2 * TN * wave + i - 2 * TM) * 1024), vb[i < 2 * TM ? 0 : i - 2 * TM], soff);
+            if (i < LA) lds_load(rA, at + (uint32_t)((LA * wave + i) * 1024), va[i < LA ? i : 0], soff);
+            else lds_load(rB, at + (uint32_t)(BM * 128 + (LB * wave + i - LA) * 1024), vb[i < LA ? 0 : i - LA], soff);
         };
 
         // fragment reads: f < TM of A, then of B; slice j of the half h of a stage
@@ -383,7 +387,7 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
     // ---- C: through LDS (this wave's quarter of the stages), so that it leaves in whole 128-byte
     // lines. Lane (m = lane % 32) holds columns 8 * (v / 4) + 4 * half + v % 4 of each 32 x 32
     // block; a row's 16-byte chunks are permuted by its number against bank conflicts.
-    char* out = smem + wave * (SCALES / 4);
+    char* out = smem + wave * (SCALES / WAVES);
     const int m0w = r.begin + wm * 32 * TM, nw = n0 + wn * 32 * TN, bytes = g.f32 ? 4 : 2;
     // Whole 16-byte pieces in every column; aligned ones leave as stores into a buffer that ends behind
     // the tile's last row, without a look at each.
@@ -398,7 +402,7 @@ __global__ __launch_bounds__(256, TM * TN == 16 || BUFS > 2 ? 1 : 2) void i8_gem
         constexpr bool F32 = decltype(f32_c)::value != 0;
         constexpr int MODE = decltype(mode_c)::value;
         constexpr int size = F32 ? 4 : 2, row_bytes = 32 * TN * size, chunks = row_bytes / 16;
-        constexpr int FIT = SCALES / 4 / (32 * row_bytes), PER = FIT >= TM ? TM : FIT >= TM / 2 ? TM / 2 : 1;  // 32-row blocks at once
+        constexpr int FIT = SCALES / WAVES / (32 * row_bytes), PER = FIT >= TM ? TM : FIT >= TM / 2 ? TM / 2 : 1;  // 32-row blocks at once
 #pragma unroll
         for (int m0 = 0; m0 < TM; m0 += PER) {
 #pragma unroll
@@ -478,23 +482,23 @@ bool launch_rows(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
 }
 
 // false: as above.
-template <int TM, int TN, int BUFS>
+template <int TM, int TN, int BUFS, int WN>
 bool launch_tile(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
-    constexpr int BM = 64 * TM, BN = 64 * TN;
+    constexpr int BM = 64 * TM, BN = 32 * WN * TN;
     const int64_t groups = most_tiles(g, BM) * ((g.N + BN - 1) / BN);
-    if (groups * 256 >= (int64_t(1) << 32)) return false;
-    hipLaunchKernelGGL((i8_gemm_tile<TM, TN, BUFS>), dim3((unsigned)groups), dim3(256), 0, stream, a);
+    if (groups * 128 * WN >= (int64_t(1) << 32)) return false;
+    hipLaunchKernelGGL((i8_gemm_tile<TM, TN, BUFS, WN>), dim3((unsigned)groups), dim3(128 * WN), 0, stream, a);
     return true;
 }
 typedef bool (*Launch)(const c3::I8Gemm&, const Args&, hipStream_t);
 
-// What a launch would take, in us: a model of where the time goes, its constants fitted to 400 shapes
+// What a launch would take, in us: a model of where the time goes, its constants fitted to 492 shapes
 // of 1 to 20000 rows, one matrix or up to 64 experts' (each kernel's times to within 7-13%, rms; what
-// it chooses is 2.5% slower than the fastest of all on average). Left out, the kernel of 16 rows would
-// cost 3% on average and up to 4x, tiles of 128x128 4%, of 64x64 2%, the others 0.5% each and up to 35%.
+// it chooses is 2.7% slower than the fastest of all on average). Left out, the kernel of 16 rows would
+// cost 2.6% on average and up to 4x, tiles of 64x64 2%, the others 0.3-1% each and up to 35%.
 // Some of the shapes (us): 198x3055x2199 rows 10.3, 64x64 6.3, 128x64 8.3, 128x128 11.3; 300x4096x4096
-// 15.1, 11.3 and 14.6 in tiles; 777x4999x4000 34, 34 and 29, 256x256 47; 4096x4096x4096 128x128 72,
-// 256x256 62; 1388x141x5565 64x64 10.5, 128x128 19.1.
+// 15.1, 11.3 and 14.6 in tiles; 1024x4096x4096 128x64 26.2, 128x128 21.2 (four stages), 24.6 (two);
+// 4096x4096x4096 128x128 74, 256x256 61; 1388x141x5565 64x64 10.5, 128x128 19.1.
 struct Model {
     const c3::I8Gemm& g;
     double n_cu, nk, used, memory;  // stages; experts with rows; the operands' and C's bytes at 6.2 TB/s
@@ -514,11 +518,11 @@ struct Model {
         const int bn = 16 * nt;
         const double per_cu = std::ceil(groups(bm, bn) / n_cu), all = per_cu * n_cu;
         const double lines = bn + std::max(2.0, std::min<double>(bm, g.M / used));
-        const double work = all * (lines * nk * 128 / 20.0e6 + bm * bn * nk * 256 / 9.0e9 + bm * bn * 1.29e-6);
+        const double work = all * (lines * nk * 128 / 20.0e6 + bm * bn * nk * 256 / 7.2e9 + bm * bn * 1.49e-6);
         const double rounds = std::max(1.0, per_cu / std::min(163840 / (2 * w * (bm + bn) * 128), 32 / w));
-        const double chain = rounds * (2.26 + nk / w * 0.0232 * (bm + bn) / 8);
+        const double chain = rounds * (2.27 + nk / w * 0.0237 * (bm + bn) / 8);
         // 1.5% less for each doubling of waves, which keep memory busier where it bounds the time
-        return (2.4 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * __builtin_ctz(w));
+        return (2.3 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * __builtin_ctz(w));
     }
     // Rounds of `slots` tiles, each a fixed part and, per stage, between `low` and `high` with the share
     // of the device that it fills.
@@ -538,18 +542,19 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
                     (int)(g.dtype == C3_F32)};
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
     const Model model(g, a.P, n_cu);
-    // 128x128: four stages in LDS where that costs no CU its second workgroup
-    Launch launch = model.groups(128, 128) <= n_cu ? launch_tile<2, 2, 4> : launch_tile<2, 2, 2>;
-    double least = model.tiles(128, 128, 2 * n_cu, 4.97, 0.272, 1.07);
+    Launch launch = launch_tile<4, 4, 2, 2>;
+    double least = model.tiles(256, 256, n_cu, 11.2, 1.01, 1.545);
     auto consider = [&](double t, Launch l) {
         if (t < least) {
             least = t;
             launch = l;
         }
     };
-    consider(model.tiles(256, 256, n_cu, 10.8, 0.967, 1.58), launch_tile<4, 4, 2>);
-    consider(model.tiles(128, 64, n_cu, 4.12, 0.231, 0.275), launch_tile<2, 1, 4>);
-    consider(model.tiles(64, 64, 2 * n_cu, 4.38, 0.114, 0.348), launch_tile<1, 1, 4>);
+    consider(model.tiles(256, 256, n_cu, 7.1, 1.034, 1.688), launch_tile<4, 2, 2, 4>);
+    consider(model.tiles(128, 128, 2 * n_cu, 4.02, 0.528, 1.174), launch_tile<2, 1, 2, 4>);
+    consider(model.tiles(128, 128, n_cu, 4.32, 0.314, 0.53), launch_tile<2, 1, 4, 4>);
+    consider(model.tiles(128, 64, n_cu, 4.03, 0.239, 0.289), launch_tile<2, 1, 4, 2>);
+    consider(model.tiles(64, 64, 2 * n_cu, 4.23, 0.116, 0.364), launch_tile<1, 1, 4, 2>);
     if (g.M <= 256 * (int64_t)model.used) {
         consider(model.rows(16, 1, 1), launch_rows<16, 1, 1>);
         consider(model.rows(16, 1, 2), launch_rows<16, 1, 2>);
@@ -560,7 +565,7 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
         consider(model.rows(32, 2, 4), launch_rows<32, 2, 4>);
         consider(model.rows(32, 2, 8), launch_rows<32, 2, 8>);
     }
-    if (!launch(g, a, stream) && !launch_tile<4, 4, 2>(g, a, stream))
+    if (!launch(g, a, stream) && !launch_tile<4, 4, 2, 2>(g, a, stream))
         return fail(C3_E_INVALID, "int8 product: too many tiles");
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;

@@ -270,17 +270,19 @@ def test_experts_loads(c3gpu, sizes):
 
 # Shapes for every kernel that the products choose from, with stages of K that are and that are not a
 # multiple of those in flight: rows of 16 and of 32 by one to eight waves, tiles of 64x64, 128x64,
-# 128x128 (a CU to itself or not) and 256x256; with experts, up to 64 of them and more.
-EVERY = [(260, 11923, 670), (261, 10960, 540), (8572, 206, 668), (8379, 198, 545), (6813, 65, 684), (5577, 66, 569),
-         (919, 9425, 669), (7812, 1171, 545), (259, 30, 670), (258, 30, 545), (1, 8263, 674), (1, 8222, 542), (1, 30, 669),
-         (1, 30, 541), (18, 8413, 681), (18, 8248, 550), (130, 902, 672), (210, 578, 545)]
-EVERY_EXPERTS = [(3167, 100, 261, 676), (3180, 100, 259, 548), (7214, 100, 135, 677), (7332, 100, 136, 567),
-                 (3813, 100, 65, 683), (4615, 70, 65, 546), (8800, 24, 946, 669), (4345, 24, 1943, 568),
-                 (8941, 70, 656, 2680), (1291, 5, 32, 717), (1327, 5, 30, 566), (101, 100, 494, 668), (83, 70, 648, 540),
-                 (105, 100, 195, 691), (113, 100, 197, 548), (2216, 100, 33, 673), (2391, 100, 33, 552),
-                 (1, 5, 30, 668), (1, 5, 30, 547), (1638, 100, 420, 668), (1914, 100, 386, 542), (805, 70, 484, 677),
-                 (904, 70, 461, 542), (2384, 100, 66, 726), (1382, 70, 115, 540), (2626, 24, 35, 691),
-                 (2508, 24, 36, 545)]
+# 128x128 (a CU to itself or not) and 256x256 (by four and by eight waves); with experts, up to 64 of
+# them and more.
+EVERY = [(260, 11923, 670), (261, 10960, 540), (8572, 206, 668), (8379, 198, 545), (7432, 68, 690), (7257, 67, 555),
+         (7219, 1030, 681), (8379, 912, 541), (8742, 1545, 3783), (8201, 1025, 5186), (259, 30, 670), (258, 30, 545),
+         (1, 8263, 674), (1, 8222, 542), (1, 30, 669), (1, 30, 541), (17, 10708, 695), (17, 11909, 544), (130, 902, 672),
+         (210, 578, 545), (6813, 65, 684), (919, 9425, 669), (18, 8413, 681)]
+EVERY_EXPERTS = [(2955, 100, 259, 689), (1982, 100, 321, 548), (3167, 100, 261, 676), (7214, 100, 135, 677),
+                 (7332, 100, 136, 567), (4675, 100, 66, 671), (4246, 100, 65, 575), (3813, 100, 65, 683), (8938, 100, 386, 735),
+                 (8915, 100, 408, 542), (8800, 24, 946, 669), (4345, 24, 1943, 568), (2521, 24, 2384, 3765),
+                 (2160, 24, 2247, 4134), (7714, 70, 645, 4129), (1291, 5, 32, 717), (1327, 5, 30, 566), (101, 100, 494, 668),
+                 (83, 70, 648, 540), (105, 100, 195, 691), (113, 100, 197, 548), (2216, 100, 33, 673), (2391, 100, 33, 552),
+                 (1, 5, 30, 668), (1, 5, 30, 547), (1638, 100, 420, 668), (793, 70, 753, 547), (805, 70, 484, 677),
+                 (904, 70, 461, 542), (1998, 100, 81, 686), (1204, 70, 131, 542), (2626, 24, 35, 691), (2508, 24, 36, 545)]
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
