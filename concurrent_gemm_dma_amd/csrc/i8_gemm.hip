@@ -206,9 +206,10 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // reads the next slice's fragments; in the last and the next stage's first it issues the loads that
 // refill the buffer, spread over the instructions (all of them in the last slice 3-5% slower).
 //
-// 256x256 comes with 4 waves, which read least from LDS and take 2% less on long K, and with 8, of which
-// one scales and stores while another still multiplies: 8192x28672x512 239 us against 270,
-// 16384 rows of 8 experts x 14336x4096 890 against 872. 128x128 with 8: 73 us against 76 on 4096x4096x4096.
+// 256x256 comes with 4 waves, which read least from LDS and take 2% less on long K (16384 rows of 8
+// experts x 14336x4096 872 us against 890), and with 8, of which one scales and stores while another
+// still multiplies (8192x28672x512 239 us against 270). 128x128 comes with 8 only: 21.2 us against 25.5
+// on 1024x4096x4096, 13.3 against 14.9 on 2000x2000x2000.
 //
 // Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
 // an eighth of K further on (sums of integers have no order), so that not all ask the same memory
