@@ -31,7 +31,7 @@ struct Args {
     const int32_t* offsets;
     int64_t ldc;
     int M, N, P;  // P: padded columns
-    int E, f32;
+    int E, f32, n_cu;
 };
 
 // The rows of C that a workgroup computes: [begin, end) of one expert.
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // reads the next slice's fragments; in the last and the next stage's first it issues the loads that
 // refill the buffer, spread over the instructions (all of them in the last slice 3-5% slower).
 //
-// 256x256 comes with 4 waves, which read least from LDS and take 2% less on long K (16384 rows of 8
+// 256x256 comes with 4 waves, which read least from LDS and take 1-4% less on long K (16384 rows of 8
 // experts x 14336x4096 872 us against 890), and with 8, of which one scales and stores while another
 // still multiplies (8192x28672x512 239 us against 270). 128x128 comes with 8 only: 21.2 us against 25.5
 // on 1024x4096x4096, 13.3 against 14.9 on 2000x2000x2000.
@@ -225,35 +225,21 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // No load leaves its array: rows past the tile's are clamped to its last one, stages past the last
 // one load the last one again into a buffer nobody reads.
 template <int TM, int TN, int BUFS, int WN>
-__global__ __launch_bounds__(128 * WN, TM * TN == 16 || BUFS > 2 || WN > 2 ? 1 : 2) void i8_gemm_tile(const Args g) {
+struct Shape {  // bytes of LDS
+    static constexpr int BM = 64 * TM, BN = 32 * WN * TN, SCALES = BUFS * (BM + BN) * 128;
+    static constexpr int LDS = SCALES + (BM + BN) * 4;
+};
+
+template <int TM, int TN, int BUFS, int WN>
+__device__ __forceinline__ void multiply_tile(const Args& g, char* smem, const Rows& r, int n0) {
     constexpr int BM = 64 * TM, BN = 32 * WN * TN, ROWS = BM + BN, WAVES = 2 * WN;
-    constexpr int STAGE = ROWS * 128, SCALES = BUFS * STAGE;
+    constexpr int STAGE = ROWS * 128, SCALES = Shape<TM, TN, BUFS, WN>::SCALES;
     constexpr int NM = TM * TN, NF = TM + TN;  // matrix instructions of a slice, fragments
     constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES, LOADS = LA + LB;  // loads of a wave and stage
-    __shared__ __attribute__((aligned(1024))) char smem[SCALES + ROWS * 4];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int tiles_n = (g.N + BN - 1) / BN;
-    int tm, tn;
-    Rows r;
-    if (g.offsets && g.E <= 64) {  // one look at the offsets gives both
-        const Share<BM> s(g, lane);
-        const int tiles_m = min(s.total, g.M / BM + min(g.E, g.M));
-        if ((int)blockIdx.x >= tiles_m * tiles_n) return;
-        map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-        r = s.pick(__builtin_amdgcn_readfirstlane(tm), 0);
-    } else {
-        const int tiles_m = count_tiles<BM>(g);
-        if ((int)blockIdx.x >= tiles_m * tiles_n) return;
-        map_tile(blockIdx.x, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
-        if (!find_rows<BM>(g, tm, r)) return;
-    }
-    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
-    r.end = __builtin_amdgcn_readfirstlane(r.end);
-    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
-    const int n0 = tn * BN;
     const int half = lane >> 5, row32 = lane & 31;
     const size_t b_base = (size_t)r.expert * g.N + n0;
     auto a_row = [&](int i) -> uint32_t { return (uint32_t)min(i, r.end - 1 - r.begin); };
@@ -467,6 +453,73 @@ __global__ __launch_bounds__(128 * WN, TM * TN == 16 || BUFS > 2 || WN > 2 ? 1 :
     }
 }
 
+// The rows and the column number of a workgroup's tile: `which` says which of all it is, or -1.
+template <int BM, typename Which>
+__device__ __forceinline__ bool find_tile(const Args& g, int tiles_n, Which which, Rows& r, int& tn) {
+    int tm;
+    if (g.offsets && g.E <= 64) {  // one look at the offsets gives both
+        const Share<BM> s(g, threadIdx.x & 63);
+        const int tiles_m = min(s.total, g.M / BM + min(g.E, g.M)), t = which(tiles_m * tiles_n);
+        if (t < 0) return false;
+        map_tile(t, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        r = s.pick(__builtin_amdgcn_readfirstlane(tm), 0);
+    } else {
+        const int tiles_m = count_tiles<BM>(g), t = which(tiles_m * tiles_n);
+        if (t < 0) return false;
+        map_tile(t, tiles_m * tiles_n, tiles_m, tiles_n, tm, tn);
+        if (!find_rows<BM>(g, tm, r)) return false;
+    }
+    r.begin = __builtin_amdgcn_readfirstlane(r.begin);
+    r.end = __builtin_amdgcn_readfirstlane(r.end);
+    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
+    tn = __builtin_amdgcn_readfirstlane(tn);
+    return true;
+}
+
+template <int TM, int TN, int BUFS, int WN>
+__global__ __launch_bounds__(128 * WN, 1) void i8_gemm_tile(const Args g) {
+    constexpr int BM = 64 * TM, BN = 32 * WN * TN;
+    __shared__ __attribute__((aligned(1024))) char smem[Shape<TM, TN, BUFS, WN>::LDS];
+    Rows r;
+    int tn;
+    auto which = [](int total) { return (int)blockIdx.x < total ? (int)blockIdx.x : -1; };
+    if (find_tile<BM>(g, (g.N + BN - 1) / BN, which, r, tn)) multiply_tile<TM, TN, BUFS, WN>(g, smem, r, tn * BN);
+}
+
+// Tiles of 256x256, as many as whole rounds of the CUs take; those of up to 128 rows are done as such.
+// The tiles of the last round, where they are half of one or fewer, go in quarters: one or two rounds of
+// those take less than one of tiles (2300x8192x4096 76 us against 96, 8192x9000x4096 280 against 289; at
+// 5/8 of a round 74 against 64). Rows of 64 experts, 16384x14336x4096, 1352 us against 1395.
+template <int TN, int WN>
+__global__ __launch_bounds__(128 * WN, 1) void i8_gemm_rounds(const Args g) {
+    static_assert(TN * WN == 8, "256 columns");
+    constexpr int LDS = Shape<4, TN, 2, WN>::LDS;
+    static_assert(Shape<2, TN, 2, WN>::LDS <= LDS && Shape<2, TN / 2, 4, WN>::LDS <= LDS, "stages of the smaller ones");
+    __shared__ __attribute__((aligned(1024))) char smem[LDS];
+    Rows r;
+    int tn, quarter = -1;
+    auto which = [&](int total) {
+        const int rest = total % g.n_cu, b = blockIdx.x;
+        const int whole = total > g.n_cu && rest <= g.n_cu / 2 ? total - rest : total;
+        if (b < whole) return b;
+        if (b - whole >= 4 * (total - whole)) return -1;
+        quarter = (b - whole) / rest;
+        return whole + (b - whole) % rest;
+    };
+    if (!find_tile<256>(g, (g.N + 255) / 256, which, r, tn)) return;
+    quarter = __builtin_amdgcn_readfirstlane(quarter);
+    if (quarter >= 0) {
+        const int n0 = tn * 256 + (quarter & 1) * 128;
+        r.begin += (quarter >> 1) * 128;
+        r.end = min(r.end, r.begin + 128);
+        if (r.begin < r.end && n0 < g.N) multiply_tile<2, TN / 2, 4, WN>(g, smem, r, n0);
+    } else if (r.end - r.begin > 128) {
+        multiply_tile<4, TN, 2, WN>(g, smem, r, tn * 256);
+    } else {
+        multiply_tile<2, TN, 2, WN>(g, smem, r, tn * 256);
+    }
+}
+
 // Most tiles of `bm` rows that the experts can need.
 int64_t most_tiles(const c3::I8Gemm& g, int bm) {
     if (!g.offsets) return (g.M + bm - 1) / bm;
@@ -491,12 +544,27 @@ bool launch_tile(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
     hipLaunchKernelGGL((i8_gemm_tile<TM, TN, BUFS, WN>), dim3((unsigned)groups), dim3(128 * WN), 0, stream, a);
     return true;
 }
+
+// false: as above. Workgroups for the quarters come on top: of one matrix as many as there will be,
+// with experts as many as any number of tiles up to the most can need.
+template <int TN, int WN>
+bool launch_rounds(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
+    const int64_t total = most_tiles(g, 256) * ((g.N + 255) / 256), n = a.n_cu, rest = total % n, whole = total - rest;
+    const int64_t groups = g.offsets                      ? whole + std::max(n, std::min(4 * rest, 2 * n))
+                           : total > n && rest <= n / 2 ? whole + 4 * rest
+                                                        : total;
+    if (groups * 128 * WN >= (int64_t(1) << 32)) return false;
+    hipLaunchKernelGGL((i8_gemm_rounds<TN, WN>), dim3((unsigned)groups), dim3(128 * WN), 0, stream, a);
+    return true;
+}
 typedef bool (*Launch)(const c3::I8Gemm&, const Args&, hipStream_t);
 
 // What a launch would take, in us: a model of where the time goes, its constants fitted to 492 shapes
-// of 1 to 20000 rows, one matrix or up to 64 experts' (each kernel's times to within 7-13%, rms; what
-// it chooses is 2.7% slower than the fastest of all on average). Left out, the kernel of 16 rows would
-// cost 2.6% on average and up to 4x, tiles of 64x64 2%, the others 0.3-1% each and up to 35%.
+// of 1 to 20000 rows, one matrix or up to 64 experts', those of tiles to 880 more (each kernel's times
+// to within 13-23%, rms; what it chooses is 1.8% slower than the fastest of all on average). Left out,
+// rows of 16 would cost 2.2% on average and up to 51%, rows of 32 0.5% and 52%, tiles of 64x64 1% and
+// 54%, 128x64 0.7% and 36%, 128x128 1-1.8% and 55%, 256x256 by 8 waves 1.8% and 42%, by 4 waves nothing
+// on average, 1-4% of the largest and 12%.
 // Some of the shapes (us): 198x3055x2199 rows 10.3, 64x64 6.3, 128x64 8.3, 128x128 11.3; 300x4096x4096
 // 15.1, 11.3 and 14.6 in tiles; 1024x4096x4096 128x64 26.2, 128x128 21.2 (four stages), 24.6 (two);
 // 4096x4096x4096 128x128 74, 256x256 61; 1388x141x5565 64x64 10.5, 128x128 19.1.
@@ -525,11 +593,36 @@ struct Model {
         // 1.5% less for each doubling of waves, which keep memory busier where it bounds the time
         return (2.3 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * __builtin_ctz(w));
     }
-    // Rounds of `slots` tiles, each a fixed part and, per stage, between `low` and `high` with the share
-    // of the device that it fills.
-    double tiles(int bm, int bn, double slots, double fixed, double low, double high) const {
-        const double n = groups(bm, bn), whole = std::floor(n / slots), rest = n - whole * slots;
-        const double t = whole * (fixed + high * nk) + (rest > 0 ? fixed + (low + (high - low) * rest / slots) * nk : 0);
+    // A round of tiles, `n` of them on n_cu CUs: a fixed part and, per stage, between `few` and `one` with
+    // the share of CUs that have one, between `more` and `two` with the share of those that have a second.
+    struct Round {
+        double fixed, few, one, more, two;
+    };
+    double round(const Round& c, double n) const {
+        const double x = n / n_cu;
+        if (x <= 0) return 0;
+        return c.fixed + (x <= 1 ? c.few + (c.one - c.few) * x : c.more + (c.two - c.more) * (x - 1)) * nk;
+    }
+    double tiles(int bm, int bn, int per_cu, const Round& c) const {
+        const double n = groups(bm, bn), slots = per_cu * n_cu, whole = std::floor(n / slots);
+        const double t = whole * round(c, slots) + round(c, n - whole * slots);
+        return std::sqrt(memory * memory + t * t);
+    }
+    // Tiles of 256x256 and the last round's quarters; tiles of up to 128 rows, which take half as long, are
+    // about half of those that experts leave partly filled.
+    double quarters(const Round& c) const {
+        double m = std::ceil(g.M / 256.0);
+        if (g.offsets) m = std::max(0.6 * used, g.M / 256.0 + 0.3 * used);
+        else if (g.M % 256 && g.M % 256 <= 128) m -= 0.4;
+        const double n = m * std::ceil(g.N / 256.0), whole = std::floor(n / n_cu), rest = n - whole * n_cu;
+        double t = whole * round(c, n_cu);
+        if (whole == 0 || rest > n_cu / 2) {
+            t += round(c, rest);
+        } else {
+            const Round q = {3.6, 0.285, 0.48, 0, 0};
+            const double full = std::floor(4 * rest / n_cu);
+            t += full * round(q, n_cu) + round(q, 4 * rest - full * n_cu);
+        }
         return std::sqrt(memory * memory + t * t);
     }
 };
@@ -539,23 +632,23 @@ struct Model {
 namespace c3 {
 
 c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
-    const Args a = {g.A, g.B, g.sA, g.sB, g.C, g.offsets, g.ldc, g.M, g.N, (int)i8_padded(g.K), g.E,
-                    (int)(g.dtype == C3_F32)};
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
+    const Args a = {g.A, g.B, g.sA, g.sB, g.C, g.offsets, g.ldc, g.M, g.N, (int)i8_padded(g.K), g.E,
+                    (int)(g.dtype == C3_F32), n_cu};
     const Model model(g, a.P, n_cu);
-    Launch launch = launch_tile<4, 4, 2, 2>;
-    double least = model.tiles(256, 256, n_cu, 11.2, 1.01, 1.545);
+    Launch launch = launch_rounds<4, 2>;
+    double least = model.quarters({11.2, 1.03, 1.55, 0, 0});
     auto consider = [&](double t, Launch l) {
         if (t < least) {
             least = t;
             launch = l;
         }
     };
-    consider(model.tiles(256, 256, n_cu, 7.1, 1.034, 1.688), launch_tile<4, 2, 2, 4>);
-    consider(model.tiles(128, 128, 2 * n_cu, 4.02, 0.528, 1.174), launch_tile<2, 1, 2, 4>);
-    consider(model.tiles(128, 128, n_cu, 4.32, 0.314, 0.53), launch_tile<2, 1, 4, 4>);
-    consider(model.tiles(128, 64, n_cu, 4.03, 0.239, 0.289), launch_tile<2, 1, 4, 2>);
-    consider(model.tiles(64, 64, 2 * n_cu, 4.23, 0.116, 0.364), launch_tile<1, 1, 4, 2>);
+    consider(model.quarters({7.4, 0.85, 1.69, 0, 0}), launch_rounds<2, 4>);
+    consider(model.tiles(128, 128, 2, {3.6, 0.475, 0.79, 0.93, 1.03}), launch_tile<2, 1, 2, 4>);
+    consider(model.tiles(128, 128, 1, {4.27, 0.34, 0.54, 0, 0}), launch_tile<2, 1, 4, 4>);
+    consider(model.tiles(128, 64, 1, {4.4, 0.24, 0.34, 0, 0}), launch_tile<2, 1, 4, 2>);
+    consider(model.tiles(64, 64, 2, {3.95, 0.11, 0.17, 0.42, 0.42}), launch_tile<1, 1, 4, 2>);
     if (g.M <= 256 * (int64_t)model.used) {
         consider(model.rows(16, 1, 1), launch_rows<16, 1, 1>);
         consider(model.rows(16, 1, 2), launch_rows<16, 1, 2>);
@@ -566,7 +659,7 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
         consider(model.rows(32, 2, 4), launch_rows<32, 2, 4>);
         consider(model.rows(32, 2, 8), launch_rows<32, 2, 8>);
     }
-    if (!launch(g, a, stream) && !launch_tile<4, 4, 2, 2>(g, a, stream))
+    if (!launch(g, a, stream) && !launch_rounds<4, 2>(g, a, stream))
         return fail(C3_E_INVALID, "int8 product: too many tiles");
     C3_HIP_TRY(hipGetLastError());
     return C3_OK;

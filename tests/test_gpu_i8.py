@@ -270,19 +270,27 @@ def test_experts_loads(c3gpu, sizes):
 
 # Shapes for every kernel that the products choose from, with stages of K that are and that are not a
 # multiple of those in flight: rows of 16 and of 32 by one to eight waves, tiles of 64x64, 128x64,
-# 128x128 (a CU to itself or not) and 256x256 (by four and by eight waves); with experts, up to 64 of
-# them and more.
+# 128x128 (a CU to itself or not) and 256x256 (by four and by eight waves, with and without tiles of up
+# to 128 rows, with and without quarters in the last round); with experts, up to 64 of them and more.
 EVERY = [(260, 11923, 670), (261, 10960, 540), (8572, 206, 668), (8379, 198, 545), (7432, 68, 690), (7257, 67, 555),
          (7219, 1030, 681), (8379, 912, 541), (8742, 1545, 3783), (8201, 1025, 5186), (259, 30, 670), (258, 30, 545),
          (1, 8263, 674), (1, 8222, 542), (1, 30, 669), (1, 30, 541), (17, 10708, 695), (17, 11909, 544), (130, 902, 672),
-         (210, 578, 545), (6813, 65, 684), (919, 9425, 669), (18, 8413, 681)]
+         (210, 578, 545), (6813, 65, 684), (919, 9425, 669), (18, 8413, 681), (259, 35525, 517), (390, 33214, 690),
+         (271, 35512, 5192), (6716, 2060, 3971), (8410, 65, 503), (8455, 66, 690), (1, 20720, 680), (1, 20720, 501),
+         (1, 8423, 797), (17, 16483, 660), (17, 17037, 3050), (17, 4176, 665), (67, 16960, 690)]
 EVERY_EXPERTS = [(2955, 100, 259, 689), (1982, 100, 321, 548), (3167, 100, 261, 676), (7214, 100, 135, 677),
                  (7332, 100, 136, 567), (4675, 100, 66, 671), (4246, 100, 65, 575), (3813, 100, 65, 683), (8938, 100, 386, 735),
                  (8915, 100, 408, 542), (8800, 24, 946, 669), (4345, 24, 1943, 568), (2521, 24, 2384, 3765),
                  (2160, 24, 2247, 4134), (7714, 70, 645, 4129), (1291, 5, 32, 717), (1327, 5, 30, 566), (101, 100, 494, 668),
                  (83, 70, 648, 540), (105, 100, 195, 691), (113, 100, 197, 548), (2216, 100, 33, 673), (2391, 100, 33, 552),
                  (1, 5, 30, 668), (1, 5, 30, 547), (1638, 100, 420, 668), (793, 70, 753, 547), (805, 70, 484, 677),
-                 (904, 70, 461, 542), (1998, 100, 81, 686), (1204, 70, 131, 542), (2626, 24, 35, 691), (2508, 24, 36, 545)]
+                 (904, 70, 461, 542), (1998, 100, 81, 686), (1204, 70, 131, 542), (2626, 24, 35, 691), (2508, 24, 36, 545),
+                 (545, 24, 4263, 3917), (2225, 5, 7654, 3847), (812, 24, 4331, 3880), (1394, 70, 1535, 3679),
+                 (3451, 100, 835, 3985), (7197, 5, 1070, 503), (627, 24, 2810, 690), (3879, 5, 4761, 559),
+                 (662, 24, 2847, 506), (2318, 100, 818, 504), (2209, 100, 740, 504), (7859, 24, 65, 507),
+                 (4931, 100, 67, 690), (172, 100, 81, 515), (24, 24, 337, 652), (1209, 100, 148, 508),
+                 (304, 24, 653, 561), (254, 24, 265, 517), (1829, 100, 33, 656), (409, 24, 711, 652),
+                 (257, 24, 2718, 542), (29, 24, 855, 501)]
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
