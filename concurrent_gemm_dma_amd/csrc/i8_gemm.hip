@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // Tile kernel
 // ------------------------------------------------------------------------------------------------
 // 2 x WN waves, each 32*TM x 32*TN of C from v_mfma_i32_32x32x32_i8 (lane l: row l % 32, 16 of the
-// slice's 32 columns): 256x256 for full devices, 128x128, 128x64 and 64x64 to have a tile for every CU.
+// slice's 32 columns): 256x256 for full devices, 128x128, 128x64, 64x64 and 64x32 to have a tile for every CU.
 // K goes in stages of 128 columns: a whole line of a row. BUFS stages are in LDS. A stage is four slices
 // of TM*TN matrix instructions, one barrier before the last. While those of one slice run, the wave
 // reads the next slice's fragments; in the last and the next stage's first it issues the loads that
@@ -209,7 +209,9 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // 256x256 comes with 4 waves, which read least from LDS and take 1-4% less on long K (16384 rows of 8
 // experts x 14336x4096 872 us against 890), and with 8, of which one scales and stores while another
 // still multiplies (8192x28672x512 239 us against 270). 128x128 comes with 8 only: 21.2 us against 25.5
-// on 1024x4096x4096, 13.3 against 14.9 on 2000x2000x2000.
+// on 1024x4096x4096, 13.3 against 14.9 on 2000x2000x2000. 64x32 for long K and too
+// few of 64x64: 128x4096x14336 29 us against 35, 64x8192x8192 19.9 and 22.7 (a CU takes in 50-60 GB/s
+// then; neither eight stages in LDS nor a whole stage's fragments in registers made it more).
 //
 // Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
 // an eighth of K further on (sums of integers have no order), so that not all ask the same memory
@@ -564,7 +566,7 @@ typedef bool (*Launch)(const c3::I8Gemm&, const Args&, hipStream_t);
 // to within 13-23%, rms; what it chooses is 1.8% slower than the fastest of all on average). Left out,
 // rows of 16 would cost 2.2% on average and up to 51%, rows of 32 0.5% and 52%, tiles of 64x64 1% and
 // 54%, 128x64 0.7% and 36%, 128x128 1-1.8% and 55%, 256x256 by 8 waves 1.8% and 42%, by 4 waves nothing
-// on average, 1-4% of the largest and 12%.
+// on average, 1-4% of the largest and 12%. 64x32 came after: up to 20%.
 // Some of the shapes (us): 198x3055x2199 rows 10.3, 64x64 6.3, 128x64 8.3, 128x128 11.3; 300x4096x4096
 // 15.1, 11.3 and 14.6 in tiles; 1024x4096x4096 128x64 26.2, 128x128 21.2 (four stages), 24.6 (two);
 // 4096x4096x4096 128x128 74, 256x256 61; 1388x141x5565 64x64 10.5, 128x128 19.1.
@@ -649,6 +651,7 @@ c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
     consider(model.tiles(128, 128, 1, {4.27, 0.34, 0.54, 0, 0}), launch_tile<2, 1, 4, 4>);
     consider(model.tiles(128, 64, 1, {4.4, 0.24, 0.34, 0, 0}), launch_tile<2, 1, 4, 2>);
     consider(model.tiles(64, 64, 2, {3.95, 0.11, 0.17, 0.42, 0.42}), launch_tile<1, 1, 4, 2>);
+    consider(model.tiles(64, 32, 2, {3.5, 0.1, 0.135, 0.3, 0.33}), launch_tile<1, 1, 4, 1>);
     if (g.M <= 256 * (int64_t)model.used) {
         consider(model.rows(16, 1, 1), launch_rows<16, 1, 1>);
         consider(model.rows(16, 1, 2), launch_rows<16, 1, 2>);

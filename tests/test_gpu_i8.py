@@ -269,7 +269,7 @@ def test_experts_loads(c3gpu, sizes):
 
 
 # Shapes for every kernel that the products choose from, with stages of K that are and that are not a
-# multiple of those in flight: rows of 16 and of 32 by one to eight waves, tiles of 64x64, 128x64,
+# multiple of those in flight: rows of 16 and of 32 by one to eight waves, tiles of 64x32, 64x64, 128x64,
 # 128x128 (a CU to itself or not) and 256x256 (by four and by eight waves, with and without tiles of up
 # to 128 rows, with and without quarters in the last round); with experts, up to 64 of them and more.
 EVERY = [(260, 11923, 670), (261, 10960, 540), (8572, 206, 668), (8379, 198, 545), (7432, 68, 690), (7257, 67, 555),
@@ -277,7 +277,10 @@ EVERY = [(260, 11923, 670), (261, 10960, 540), (8572, 206, 668), (8379, 198, 545
          (1, 8263, 674), (1, 8222, 542), (1, 30, 669), (1, 30, 541), (17, 10708, 695), (17, 11909, 544), (130, 902, 672),
          (210, 578, 545), (6813, 65, 684), (919, 9425, 669), (18, 8413, 681), (259, 35525, 517), (390, 33214, 690),
          (271, 35512, 5192), (6716, 2060, 3971), (8410, 65, 503), (8455, 66, 690), (1, 20720, 680), (1, 20720, 501),
-         (1, 8423, 797), (17, 16483, 660), (17, 17037, 3050), (17, 4176, 665), (67, 16960, 690)]
+         (1, 8423, 797), (17, 16483, 660), (17, 17037, 3050), (17, 4176, 665), (67, 16960, 690),
+         (132, 14566, 508), (68, 16577, 851), (6555, 129, 899), (75, 8259, 1038), (65, 8813, 648), (68, 8201, 863),
+         (9, 8308, 500), (17, 8436, 781), (1, 30, 1823), (18, 16388, 1040), (18, 18784, 3156), (17, 4119, 4295),
+         (17, 4239, 3199)]
 EVERY_EXPERTS = [(2955, 100, 259, 689), (1982, 100, 321, 548), (3167, 100, 261, 676), (7214, 100, 135, 677),
                  (7332, 100, 136, 567), (4675, 100, 66, 671), (4246, 100, 65, 575), (3813, 100, 65, 683), (8938, 100, 386, 735),
                  (8915, 100, 408, 542), (8800, 24, 946, 669), (4345, 24, 1943, 568), (2521, 24, 2384, 3765),
@@ -290,7 +293,17 @@ EVERY_EXPERTS = [(2955, 100, 259, 689), (1982, 100, 321, 548), (3167, 100, 261, 
                  (662, 24, 2847, 506), (2318, 100, 818, 504), (2209, 100, 740, 504), (7859, 24, 65, 507),
                  (4931, 100, 67, 690), (172, 100, 81, 515), (24, 24, 337, 652), (1209, 100, 148, 508),
                  (304, 24, 653, 561), (254, 24, 265, 517), (1829, 100, 33, 656), (409, 24, 711, 652),
-                 (257, 24, 2718, 542), (29, 24, 855, 501)]
+                 (257, 24, 2718, 542), (29, 24, 855, 501),
+                 (506, 24, 1366, 506), (118, 5, 6558, 522), (886, 24, 1190, 518), (147, 5, 6517, 642),
+                 (754, 24, 1251, 772), (7356, 100, 147, 503), (7269, 100, 131, 778), (1277, 24, 453, 912),
+                 (908, 24, 554, 1043), (7322, 24, 98, 655), (7337, 24, 98, 823), (4821, 100, 105, 906),
+                 (4639, 100, 98, 1025), (7318, 100, 66, 1178), (5517, 70, 104, 837), (57, 5, 1713, 505),
+                 (7290, 24, 33, 709), (7272, 24, 34, 801), (4358, 100, 33, 507), (5620, 70, 33, 790),
+                 (1, 70, 30, 770), (29, 24, 2254, 511), (26, 24, 2447, 530), (6, 5, 5093, 514), (7, 5, 1654, 1027),
+                 (74, 70, 114, 908), (1, 5, 33, 1671), (6, 5, 30, 1556), (32, 70, 30, 1414), (12, 70, 31, 1552),
+                 (1423, 100, 643, 508), (1040, 70, 1009, 528), (397, 24, 1355, 515), (280, 24, 664, 976),
+                 (268, 24, 663, 1073), (1153, 100, 145, 905), (905, 70, 197, 1057), (413, 24, 199, 2742),
+                 (192, 24, 309, 2654), (1928, 100, 34, 3044), (1112, 100, 51, 2317)]
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
