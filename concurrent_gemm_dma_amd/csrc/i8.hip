@@ -6,6 +6,7 @@
 // that one rounding to an integer, which stands in the low byte.
 #include "c3_internal.h"
 #include "pieces.h"
+#include "places.h"
 #include "row_io.h"
 
 namespace {
@@ -51,7 +52,37 @@ struct Args {
     int32_t* pos;
     int64_t ld, cols, first, rows, padded;  // `rows` rows from `first` on
     int T, top_k, E, S;
+    int check;  // BY_TOKEN: the first workgroups, which write the rows of slots that order names again
 };
+
+// A row's factor and scale, from the bits of its largest magnitude.
+struct Unit {
+    bool bad;  // an infinity or NaN among its values
+    float r, scale;
+    __device__ __forceinline__ Unit(uint32_t m) {
+        bad = m >= 0x7F800000u;
+        const float a = fmaxf(__builtin_bit_cast(float, m), 0x1p-119f);
+        r = 127.f / a;
+        scale = bad ? __builtin_nanf("") : a / 127.f;
+    }
+};
+
+// A wave quantises row `from` of x to row `to` of the operand, reading it twice.
+template <bool BF16>
+__device__ __forceinline__ void quantize_by_wave(const Args& g, int64_t from, int64_t to) {
+    constexpr int SIZE = BF16 ? 2 : 4;
+    const char* x = g.x + from * g.ld * SIZE;
+    const uint32_t lane = threadIdx.x & 63, pieces = (uint32_t)(g.padded / 8);
+    auto load = [&](uint32_t c) { return load_eight<BF16, false>(x + (int64_t)c * 8 * SIZE, g.cols - (int64_t)c * 8); };
+    uint32_t m = 0;
+    for (uint32_t c = lane; c < pieces; c += 64) m = max(m, largest<BF16>(load(c)));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    const Unit unit(m);
+    if (lane == 0) g.scales[to] = unit.scale;
+    u32x2_t* codes = reinterpret_cast<u32x2_t*>(g.codes + to * g.padded);
+    for (uint32_t c = lane; c < pieces; c += 64) codes[c] = encode<BF16>(load(c), unit.r, unit.bad);
+}
 
 // G lanes take a row, eight values a piece, the first U pieces of a lane in registers; what is past
 // them is read twice.
@@ -60,12 +91,19 @@ __global__ __launch_bounds__(G > kThreads ? G : kThreads) void quantize_rows(con
     constexpr int PER = G > kThreads ? 1 : kThreads / G, SIZE = BF16 ? 2 : 4, WAVES = G / 64;
     constexpr bool ONCE = MODE != BY_ROW;
     const int lane = threadIdx.x % G;
-    const int64_t i = (int64_t)blockIdx.x * PER + threadIdx.x / G;
+    int n = 0;
+    if constexpr (MODE != PLAIN) n = min(max(g.offsets[g.E], 0), g.S);
+    if constexpr (MODE == BY_TOKEN) {
+        if ((int)blockIdx.x < g.check) {
+            c3::each_other_place(g, n, g.check, [&](int p, int slot) { quantize_by_wave<BF16>(g, slot % g.T, p); });
+            return;
+        }
+    }
+    const int64_t group = MODE == BY_TOKEN ? blockIdx.x - g.check : blockIdx.x;
+    const int64_t i = group * PER + threadIdx.x / G;
     bool here = i < g.rows;
     const int64_t row = g.first + (here ? i : 0);
     int64_t from = row;
-    int n = 0;
-    if constexpr (MODE != PLAIN) n = min(max(g.offsets[g.E], 0), g.S);
     if constexpr (MODE == BY_ROW) {
         const int slot = here ? g.order[row] : -1;
         here = slot >= 0 && slot < g.S;
@@ -97,24 +135,26 @@ __global__ __launch_bounds__(G > kThreads ? G : kThreads) void quantize_rows(con
         for (int w = 0; w < WAVES; ++w) m = max(m, part[w0 + w]);
     }
     if (!here) return;
-    const bool bad = m >= 0x7F800000u;  // an infinity or NaN among them
-    const float a = fmaxf(__builtin_bit_cast(float, m), 0x1p-119f);
-    const float r = 127.f / a, scale = bad ? __builtin_nanf("") : a / 127.f;
+    const Unit unit(m);
     auto store = [&](int64_t to) {
         u32x2_t* codes = reinterpret_cast<u32x2_t*>(g.codes + to * g.padded);
-        if (lane == 0) g.scales[to] = scale;
+        if (lane == 0) g.scales[to] = unit.scale;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t c = lane + u * G;
-            if (c < pieces) codes[c] = encode<BF16>(v[u], r, bad);
+            if (c < pieces) codes[c] = encode<BF16>(v[u], unit.r, unit.bad);
         }
         for (uint32_t c = lane + U * G; c < pieces; c += G)
-            codes[c] = encode<BF16>(load_eight<BF16, false>(x + (int64_t)c * 8 * SIZE, fit(c)), r, bad);
+            codes[c] = encode<BF16>(load_eight<BF16, false>(x + (int64_t)c * 8 * SIZE, fit(c)), unit.r, unit.bad);
     };
     if constexpr (MODE == BY_TOKEN) {
-        for (int j = 0; j < g.top_k; ++j) {
-            const int p = g.pos[(int64_t)j * g.T + row];
-            if (p >= 0 && p < n) store(p);
+        constexpr int B = 16;  // places looked up together, one a lane
+        for (int j0 = 0; j0 < g.top_k; j0 += B) {
+            const int mine = c3::place_of(g, n, (int)row, j0 + lane % B);
+            for (int b = 0; b < B && j0 + b < g.top_k; ++b) {
+                const int p = __shfl(mine, b, B);
+                if (p >= 0) store(p);
+            }
         }
     } else {
         store(row);
@@ -147,11 +187,12 @@ template <bool BF16, int G, int U, int MODE>
 c3_status launch(Args a, hipStream_t stream) {
     constexpr int threads = std::max(G, kThreads), per = threads / G;
     const int64_t rows = a.rows;
-    return c3::in_parts(rows, ((int64_t(1) << 32) / threads - 1) * per, [&](int64_t r, int64_t n) {
+    return c3::in_parts(rows, ((int64_t(1) << 32) / threads - 1 - c3::kMostChecks) * per, [&](int64_t r, int64_t n) {
         a.first = r;
         a.rows = n;
-        hipLaunchKernelGGL((quantize_rows<BF16, G, U, MODE>), dim3((unsigned)((n + per - 1) / per)), dim3(threads),
-                           0, stream, a);
+        a.check = MODE != BY_TOKEN || r ? 0 : c3::check_groups(a.S, threads);
+        hipLaunchKernelGGL((quantize_rows<BF16, G, U, MODE>), dim3((unsigned)((n + per - 1) / per + a.check)),
+                           dim3(threads), 0, stream, a);
     });
 }
 

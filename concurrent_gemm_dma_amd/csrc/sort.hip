@@ -6,6 +6,7 @@
 // lanes; a lane finds its row's places itself (lanes of one row read the same word).
 #include "c3_internal.h"
 #include "pieces.h"
+#include "places.h"
 #include "row_io.h"
 
 namespace {
@@ -51,27 +52,60 @@ __global__ __launch_bounds__(kThreads) void positions(const Plan g) {
     if (slot >= 0 && slot < g.S) g.pos[slot] = p < present(g) ? (int)p : -1;
 }
 
-// A lane copies a piece of token t to each of its rows: x is read once. Stores go past the caches
-// (ONCE) where a token has few rows: 32768 tokens of 4096 bf16, one choice each, 92 us against 98, but
-// with eight 476 against 446 (5.4 TB/s), written lines waiting in the caches for their neighbours.
-template <int SIZE, bool ONCE>
+// A lane copies a piece of token t to each of its rows: x is read once. A slot has the row that pos
+// says only if order says so too (places.h); the first `check` workgroups write the rows of slots that
+// order names again. Stores go past the caches (ONCE) where a token has few rows: 32768 tokens of 4096
+// bf16, one choice each, 97 us against 106, but with eight 482 against 445 (5.4 TB/s), written lines
+// waiting in the caches for their neighbours.
+// Lanes look places up for themselves, or SHARE them through LDS where a workgroup has many tokens:
+// 4000 tokens of 1000 bf16, eight choices, 15.7 us against 16.8, but 8192 of 4096, four choices, 67
+// against 63.5, two barriers for one token or two.
+template <int SIZE, bool ONCE, bool SHARE>
 __global__ __launch_bounds__(kThreads) void dispatch_by_token(const Plan g, int64_t first_row, int64_t rows,
                                                               const char* __restrict__ x, int64_t ld_x,
                                                               char* __restrict__ y, int64_t ld_y, int64_t cols,
-                                                              uint32_t per_row, uint32_t magic) {
-    constexpr int B = 4;  // places in flight together
-    const At at = locate((int64_t)blockIdx.x * kThreads, threadIdx.x, per_row, magic);
-    if (at.row >= rows) return;
-    const int64_t t = first_row + at.row, c = (int64_t)at.piece * kValues<SIZE>;
+                                                              uint32_t per_row, uint32_t magic, int check) {
+    constexpr int B = SHARE && !ONCE ? 8 : 4;  // places looked up together
     const int n = present(g);
-    const u32x4_t v = load_piece<SIZE, true>(x + (t * ld_x + c) * SIZE, cols - c);
-    for (int j0 = 0; j0 < g.top_k; j0 += B) {
-        int p[B];
+    if ((int)blockIdx.x < check) {
+        c3::each_other_place(g, n, check, [&](int p, int slot) {
+            const char* from = x + (int64_t)(slot % g.T) * ld_x * SIZE;
+            char* to = y + (int64_t)p * ld_y * SIZE;
+            for (int64_t c = (threadIdx.x & 63) * kValues<SIZE>; c < cols; c += 64 * kValues<SIZE>)
+                store_piece<SIZE, false>(to + c * SIZE, load_piece<SIZE, false>(from + c * SIZE, cols - c), cols - c);
+        });
+        return;
+    }
+    const int64_t first = (int64_t)(blockIdx.x - check) * kThreads;
+    const At at = locate(first, threadIdx.x, per_row, magic);
+    const int64_t t = first_row + at.row, c = (int64_t)at.piece * kValues<SIZE>;
+    const bool here = at.row < rows;
+    if (!SHARE && !here) return;
+    u32x4_t v = {};
+    if (here) v = load_piece<SIZE, true>(x + (t * ld_x + c) * SIZE, cols - c);
+    auto store = [&](int p) {
+        if (p >= 0) store_piece<SIZE, ONCE>(y + ((int64_t)p * ld_y + c) * SIZE, v, cols - c);
+    };
+    if constexpr (SHARE) {
+        __shared__ int place[B][kThreads];  // of the workgroup's tokens, row0 on
+        const int64_t row0 = locate(first, 0, per_row, magic).row;
+        const int tokens = (int)(min(locate(first, kThreads - 1, per_row, magic).row, rows - 1) - row0) + 1;
+        for (int j0 = 0; j0 < g.top_k; j0 += B) {
+            for (int i = threadIdx.x; i < tokens * B; i += kThreads)
+                place[i % B][i / B] = c3::place_of(g, n, (int)(first_row + row0) + i / B, j0 + i % B);
+            __syncthreads();
 #pragma unroll
-        for (int b = 0; b < B; ++b) p[b] = j0 + b < g.top_k ? g.pos[(int64_t)(j0 + b) * g.T + t] : -1;
+            for (int b = 0; b < B; ++b)
+                if (here) store(place[b][at.row - row0]);
+            __syncthreads();
+        }
+    } else {
+        for (int j0 = 0; j0 < g.top_k; j0 += B) {
+            int p[B];
+            c3::places_of<B>(g, n, (int)t, j0, p);
 #pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (p[b] >= 0 && p[b] < n) store_piece<SIZE, ONCE>(y + ((int64_t)p[b] * ld_y + c) * SIZE, v, cols - c);
+            for (int b = 0; b < B; ++b) store(p[b]);
+        }
     }
 }
 
@@ -177,9 +211,11 @@ Plan plan_of(const c3::SortArgs& a) {
     return {a.order, a.offsets, a.pos, (int)a.T, a.top_k, a.E, (int)(a.T * a.top_k)};
 }
 
-// Rows of `per_row` pieces that one launch takes (per_row < 2^29).
+// Rows of `per_row` pieces that one launch takes beside `others` workgroups (per_row < 2^29).
 constexpr int64_t kMostGroups = (int64_t(1) << 32) / kThreads - 1;
-int64_t most_rows(uint32_t per_row) { return std::max<int64_t>(1, kMostGroups * kThreads / per_row); }
+int64_t most_rows(uint32_t per_row, int others = 0) {
+    return std::max<int64_t>(1, (kMostGroups - others) * kThreads / per_row);
+}
 dim3 groups_of(int64_t rows, uint32_t per_row) {
     return dim3((unsigned)((rows * per_row + kThreads - 1) / kThreads));
 }
@@ -196,14 +232,21 @@ c3_status dispatch(const c3::SortArgs& a, hipStream_t stream) {
     const uint32_t per_row = pieces_of<SIZE>(a.cols), magic = c3::magic_of(per_row);
     const char* x = static_cast<const char*>(a.x);
     char* y = static_cast<char*>(a.out);
-    const bool tokens = c3::by_token(a);
-    if (tokens) C3_TRY(c3::positions_enqueue(a, stream));
-    auto kernel = !tokens       ? dispatch_by_row<SIZE>
-                  : a.top_k > 4 ? dispatch_by_token<SIZE, false>
-                                : dispatch_by_token<SIZE, true>;
-    return c3::in_parts(tokens ? a.T : g.S, most_rows(per_row), [&](int64_t r, int64_t n) {
-        hipLaunchKernelGGL(kernel, groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n, x, a.ld_x, y, a.ld_out,
-                           a.cols, per_row, magic);
+    if (!c3::by_token(a))
+        return c3::in_parts(g.S, most_rows(per_row), [&](int64_t r, int64_t n) {
+            hipLaunchKernelGGL(dispatch_by_row<SIZE>, groups_of(n, per_row), dim3(kThreads), 0, stream, g, r, n, x,
+                               a.ld_x, y, a.ld_out, a.cols, per_row, magic);
+        });
+    C3_TRY(c3::positions_enqueue(a, stream));
+    const bool share = per_row <= kThreads;
+    auto kernel = a.top_k > 4 ? (share ? dispatch_by_token<SIZE, false, true> : dispatch_by_token<SIZE, false, false>)
+                              : (share ? dispatch_by_token<SIZE, true, true> : dispatch_by_token<SIZE, true, false>);
+    return c3::in_parts(a.T, most_rows(per_row, c3::kMostChecks), [&](int64_t r, int64_t n) {
+        const int check = r ? 0 : c3::check_groups(g.S, kThreads);
+        dim3 groups = groups_of(n, per_row);
+        groups.x += check;
+        hipLaunchKernelGGL(kernel, groups, dim3(kThreads), 0, stream, g, r, n, x, a.ld_x, y, a.ld_out, a.cols, per_row,
+                           magic, check);
     });
 }
 
@@ -252,12 +295,16 @@ c3_status gradient(const c3::SortArgs& a, hipStream_t stream) {
 namespace c3 {
 
 // Rows by token where reading x again for every choice costs more than the launch that turns the
-// order round. Sorted by row and by token, 4096 bf16 and four choices: 256 tokens 5.3 and 8.0 us, 1024
-// tokens (67 MB read and written) 12.2 and 10.4; quantised 6.4 and 7.0, 14.4 and 9.4 (50 MB); 32768
-// tokens of eight choices 718 and 446.
+// order round and looking places up, and in batches past the caches, where x is read in order. Sorted by
+// row and by token: 12000 tokens of 1000 bf16, two choices (24 MB read again), 16.7 and 19.1 us; 1500 of
+// 4096, three (25 MB), 12.1 and 12.5; 1024 of 4096, four (25 MB), 10.8 and 10.5; 3000 of 1000, six (30
+// MB), 12.5 and 11.4; 32768 of 4096, eight (1.9 GB), 720 and 444; with one choice 8192 of 4096 (134 MB
+// in all) 27.9 and 29.0, 32768 (537 MB) 103 and 98. Quantised, 1024 of 4096, four, 9.6 and 9.5; 20000 of
+// 200, six, 16.0 and 13.2; 32768 of 4096, eight, 456 and 265.
 bool by_token(const SortArgs& a) {
     const double size = a.dtype == C3_BF16 ? 2 : 4, values = (double)a.T * a.top_k * a.cols;
-    return a.scales ? values * (size + 1) > 20e6 : values * 2 * size > 48e6;
+    if (a.scales) return values * (size + 1) > 20e6;
+    return (values - (double)a.T * a.cols) * size > 25e6 || values * 2 * size > kLarge;
 }
 
 c3_status positions_enqueue(const SortArgs& a, hipStream_t stream) {

@@ -511,7 +511,8 @@ c3_status c3_mx4_gemm_experts(const void* A, const void* sA, int64_t a_rows, con
 /* Sort rows by expert, the send buffer of an all-to-all: y[p] = x[order[p] % n_tokens] for p < n.
  * x[n_tokens][ld], y[n_tokens * top_k][ld_y] (dtype); rows n.. of y are left as they were.
  * pos[n_tokens * top_k]: slot s is row pos[s] of y, or -1 without an expert: what c3_combine reads.
- * Where order is not c3_route_plan's, slots it does not name keep their old pos.
+ * Where order is not c3_route_plan's, slots it does not name keep their old pos, and of a slot that
+ * it names more than once pos holds one of its places, whichever (y has them all).
  * Its gradient is c3_combine without weights. n_tokens = 0 is a no-op; cols >= 1. */
 c3_status c3_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_t cols, int64_t ld,
                       const int32_t* order, const int32_t* offsets, int top_k, int n_experts,
