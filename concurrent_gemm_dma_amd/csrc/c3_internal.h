@@ -45,10 +45,13 @@ void clear_error();
         if (st_ != C3_OK) return st_;     \
     } while (0)
 
-// Body of an entry point: takes the library mutex and turns C++ exceptions into a status.
+// Body of an entry point: takes the library mutex, makes the library's device the current one for the
+// call, and turns C++ exceptions into a status.
 #define C3_ENTRY(body)                                                      \
     try {                                                                   \
         std::lock_guard<std::recursive_mutex> lock_(api_mutex());           \
+        ::c3::OnDevice on_device_;                                          \
+        C3_TRY(on_device_.enter());                                         \
         body                                                                \
     } catch (const std::exception& e) {                                     \
         return fail(C3_E_INVALID, "internal exception: %s", e.what());      \
@@ -69,6 +72,24 @@ struct Context {
 Context& ctx();
 std::recursive_mutex& api_mutex();
 c3_status require_init();
+
+// The library's device is the current one for as long as this lives, whichever was before: streams,
+// launches and allocations go to the current device. Nothing is done as long as there is none.
+struct OnDevice {
+    int before = -1;
+    c3_status enter() {
+        if (!ctx().inited) return C3_OK;
+        int now = 0;
+        C3_HIP_TRY(hipGetDevice(&now));
+        if (now == ctx().device) return C3_OK;
+        C3_HIP_TRY(hipSetDevice(ctx().device));
+        before = now;
+        return C3_OK;
+    }
+    ~OnDevice() {
+        if (before >= 0) (void)hipSetDevice(before);
+    }
+};
 
 // ---- argument checks --------------------------------------------------------------------------
 c3_status check_device_ptr(const void* p, size_t bytes, const char* what);

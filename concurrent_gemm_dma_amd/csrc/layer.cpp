@@ -163,22 +163,6 @@ size_t codes_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (mx4_padd
 size_t scales_bytes(int64_t rows, int64_t cols) { return (size_t)rows * (mx4_padded(cols) / 32); }
 size_t i8_bytes(int64_t rows, int64_t cols) { return (size_t)rows * i8_padded(cols); }
 
-// The library's device is the current one for as long as this lives, whichever was before.
-struct OnDevice {
-    int before = -1;
-    c3_status enter() {
-        int now = 0;
-        C3_HIP_TRY(hipGetDevice(&now));
-        if (now == ctx().device) return C3_OK;
-        C3_HIP_TRY(hipSetDevice(ctx().device));
-        before = now;
-        return C3_OK;
-    }
-    ~OnDevice() {
-        if (before >= 0) (void)hipSetDevice(before);
-    }
-};
-
 c3_status check_cols(const char* who, int64_t cols) {
     if (cols < 1 || cols >= (int64_t(1) << 31))
         return fail(C3_E_INVALID, "%s: cols must be in [1, 2^31), got %lld", who, (long long)cols);
@@ -511,8 +495,6 @@ c3_status c3_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_t c
         a.pos = pos;
         a.out = y;
         a.ld_out = ld_y;
-        OnDevice device;
-        C3_TRY(device.enter());
         return dispatch_enqueue(a, static_cast<hipStream_t>(stream));
     })
 }
@@ -546,8 +528,6 @@ c3_status c3_combine(const void* y, c3_dtype dtype, int64_t n_tokens, int top_k,
         a.weights = weights;
         a.out = out;
         a.ld_out = ld_out;
-        OnDevice device;
-        C3_TRY(device.enter());
         return combine_enqueue(a, static_cast<hipStream_t>(stream));
     })
 }
@@ -589,8 +569,6 @@ c3_status c3_combine_backward(const void* dout, c3_dtype dtype, int64_t n_tokens
         a.out = dy;
         a.ld_out = ld_dy;
         a.dweights = dweights;
-        OnDevice device;
-        C3_TRY(device.enter());
         return combine_backward_enqueue(a, static_cast<hipStream_t>(stream));
     })
 }
@@ -627,8 +605,6 @@ c3_status c3_i8_quantize(const void* x, c3_dtype dtype, int64_t rows, int64_t co
         a.ld_x = ld;
         a.out = codes;
         a.scales = scales;
-        OnDevice device;
-        C3_TRY(device.enter());
         return i8_quantize_enqueue(a, static_cast<hipStream_t>(stream));
     })
 }
@@ -666,8 +642,6 @@ c3_status c3_i8_dispatch(const void* x, c3_dtype dtype, int64_t n_tokens, int64_
         a.pos = pos;
         a.out = codes;
         a.scales = scales;
-        OnDevice device;
-        C3_TRY(device.enter());
         return i8_quantize_enqueue(a, static_cast<hipStream_t>(stream));
     })
 }
@@ -685,8 +659,6 @@ c3_status c3_i8_dequantize(const void* codes, const float* scales, int64_t rows,
         C3_TRY(check_arrays(who, {{codes, i8_bytes(rows, cols), 16, "codes", false},
                                   {scales, (size_t)rows * 4, 4, "scales", false},
                                   {y, strided_bytes(rows, cols, ld, size), size, "y", true}}));
-        OnDevice device;
-        C3_TRY(device.enter());
         return i8_dequantize_enqueue(codes, scales, rows, cols, y, dtype, ld,
                                      static_cast<hipStream_t>(stream));
     })
@@ -719,8 +691,6 @@ c3_status c3_i8_gemm(const void* A, const float* sA, const void* B, const float*
         g.N = (int)N;
         g.K = (int)K;
         g.ldc = ldc;
-        OnDevice device;
-        C3_TRY(device.enter());
         return i8_gemm_enqueue(g, static_cast<hipStream_t>(stream));
     })
 }
@@ -759,8 +729,6 @@ c3_status c3_i8_gemm_experts(const void* A, const float* sA, const void* B, cons
         g.ldc = ldc;
         g.offsets = offsets;
         g.E = n_experts;
-        OnDevice device;
-        C3_TRY(device.enter());
         return i8_gemm_enqueue(g, static_cast<hipStream_t>(stream));
     })
 }

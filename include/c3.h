@@ -24,6 +24,8 @@
  *     never frees them. Host pointers are only accepted where a parameter says "host".
  *   - A `stream` parameter is a hipStream_t passed as void*; NULL means the null stream.
  *   - Sizes are in bytes unless named M, N, K (elements).
+ *   - Calls run on the device passed to c3_init whichever device is current, and leave that one
+ *     current (the first c3_init makes its own current). A stream has to be of that device.
  *   - Calls are serialized by one internal mutex. Kernel faults surface asynchronously at the
  *     next synchronizing call, as in HIP.
  */
