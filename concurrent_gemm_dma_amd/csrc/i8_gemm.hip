@@ -11,9 +11,8 @@
 // Rows past M or N read a valid row instead (their results are not stored); columns need no mask,
 // since operands are padded with zeros to a multiple of 128.
 #include "c3_internal.h"
+#include "i8_choice.h"
 #include "tile_util.h"
-
-#include <cmath>
 
 namespace {
 
@@ -553,81 +552,20 @@ template <int TN, int WN>
 bool launch_rounds(const c3::I8Gemm& g, const Args& a, hipStream_t stream) {
     const int64_t total = most_tiles(g, 256) * ((g.N + 255) / 256), n = a.n_cu, rest = total % n, whole = total - rest;
     const int64_t groups = g.offsets                      ? whole + std::max(n, std::min(4 * rest, 2 * n))
-                           : total > n && rest <= n / 2 ? whole + 4 * rest
-                                                        : total;
+                           : c3::i8::in_quarters(total, n) ? whole + 4 * rest
+                                                           : total;
     if (groups * 128 * WN >= (int64_t(1) << 32)) return false;
     hipLaunchKernelGGL((i8_gemm_rounds<TN, WN>), dim3((unsigned)groups), dim3(128 * WN), 0, stream, a);
     return true;
 }
 typedef bool (*Launch)(const c3::I8Gemm&, const Args&, hipStream_t);
 
-// What a launch would take, in us: a model of where the time goes, its constants fitted to 492 shapes
-// of 1 to 20000 rows, one matrix or up to 64 experts', those of tiles to 880 more (each kernel's times
-// to within 13-23%, rms; what it chooses is 1.8% slower than the fastest of all on average). Left out,
-// rows of 16 would cost 2.2% on average and up to 51%, rows of 32 0.5% and 52%, tiles of 64x64 1% and
-// 54%, 128x64 0.7% and 36%, 128x128 1-1.8% and 55%, 256x256 by 8 waves 1.8% and 42%, by 4 waves nothing
-// on average, 1-4% of the largest and 12%. 64x32 came after: up to 20%.
-// Some of the shapes (us): 198x3055x2199 rows 10.3, 64x64 6.3, 128x64 8.3, 128x128 11.3; 300x4096x4096
-// 15.1, 11.3 and 14.6 in tiles; 1024x4096x4096 128x64 26.2, 128x128 21.2 (four stages), 24.6 (two);
-// 4096x4096x4096 128x128 74, 256x256 61; 1388x141x5565 64x64 10.5, 128x128 19.1.
-struct Model {
-    const c3::I8Gemm& g;
-    double n_cu, nk, used, memory;  // stages; experts with rows; the operands' and C's bytes at 6.2 TB/s
-    Model(const c3::I8Gemm& g_, int P, int n_cu_) : g(g_), n_cu(n_cu_), nk(P / 128), used(std::min(g_.E, g_.M)) {
-        const double reached = g.offsets ? g.E * (1.0 - std::pow(1.0 - 1.0 / g.E, g.M)) : 1.0;
-        const double size = g.dtype == C3_F32 ? 4 : 2;
-        memory = (reached * g.N * P + (double)g.M * P + (double)g.M * g.N * size) / 6.2e6;
-    }
-    // Workgroups; loads of experts are not known on the host, each leaves a tile partly filled.
-    double groups(int bm, int bn) const {
-        const double m = g.offsets ? std::max(used, g.M / (double)bm + 0.6 * used) : std::ceil(g.M / (double)bm);
-        return m * std::ceil(g.N / (double)bn);
-    }
-    // Memory, the way from L2 through LDS with the matrix instructions and the sums, and the chain of a
-    // workgroup's start and stages, none of which hides the others wholly. The fullest CU counts.
-    double rows(int bm, int nt, int w) const {
-        const int bn = 16 * nt;
-        const double per_cu = std::ceil(groups(bm, bn) / n_cu), all = per_cu * n_cu;
-        const double lines = bn + std::max(2.0, std::min<double>(bm, g.M / used));
-        const double work = all * (lines * nk * 128 / 20.0e6 + bm * bn * nk * 256 / 7.2e9 + bm * bn * 1.49e-6);
-        const double rounds = std::max(1.0, per_cu / std::min(163840 / (2 * w * (bm + bn) * 128), 32 / w));
-        const double chain = rounds * (2.27 + nk / w * 0.0237 * (bm + bn) / 8);
-        // 1.5% less for each doubling of waves, which keep memory busier where it bounds the time
-        return (2.3 + std::sqrt(memory * memory + work * work + chain * chain)) * (1 - 0.015 * __builtin_ctz(w));
-    }
-    // A round of tiles, `n` of them on n_cu CUs: a fixed part and, per stage, between `few` and `one` with
-    // the share of CUs that have one, between `more` and `two` with the share of those that have a second.
-    struct Round {
-        double fixed, few, one, more, two;
-    };
-    double round(const Round& c, double n) const {
-        const double x = n / n_cu;
-        if (x <= 0) return 0;
-        return c.fixed + (x <= 1 ? c.few + (c.one - c.few) * x : c.more + (c.two - c.more) * (x - 1)) * nk;
-    }
-    double tiles(int bm, int bn, int per_cu, const Round& c) const {
-        const double n = groups(bm, bn), slots = per_cu * n_cu, whole = std::floor(n / slots);
-        const double t = whole * round(c, slots) + round(c, n - whole * slots);
-        return std::sqrt(memory * memory + t * t);
-    }
-    // Tiles of 256x256 and the last round's quarters; tiles of up to 128 rows, which take half as long, are
-    // about half of those that experts leave partly filled.
-    double quarters(const Round& c) const {
-        double m = std::ceil(g.M / 256.0);
-        if (g.offsets) m = std::max(0.6 * used, g.M / 256.0 + 0.3 * used);
-        else if (g.M % 256 && g.M % 256 <= 128) m -= 0.4;
-        const double n = m * std::ceil(g.N / 256.0), whole = std::floor(n / n_cu), rest = n - whole * n_cu;
-        double t = whole * round(c, n_cu);
-        if (whole == 0 || rest > n_cu / 2) {
-            t += round(c, rest);
-        } else {
-            const Round q = {3.6, 0.285, 0.48, 0, 0};
-            const double full = std::floor(4 * rest / n_cu);
-            t += full * round(q, n_cu) + round(q, 4 * rest - full * n_cu);
-        }
-        return std::sqrt(memory * memory + t * t);
-    }
-};
+// By c3::i8::Kernel.
+constexpr Launch kLaunch[c3::i8::KERNELS] = {
+    launch_rounds<4, 2>,     launch_rounds<2, 4>,     launch_tile<2, 1, 2, 4>, launch_tile<2, 1, 4, 4>,
+    launch_tile<2, 1, 4, 2>, launch_tile<1, 1, 4, 2>, launch_tile<1, 1, 4, 1>, launch_rows<16, 1, 1>,
+    launch_rows<16, 1, 2>,   launch_rows<16, 1, 4>,   launch_rows<16, 1, 8>,   launch_rows<32, 2, 1>,
+    launch_rows<32, 2, 2>,   launch_rows<32, 2, 4>,   launch_rows<32, 2, 8>};
 
 }  // namespace
 
@@ -635,33 +573,9 @@ namespace c3 {
 
 c3_status i8_gemm_enqueue(const I8Gemm& g, hipStream_t stream) {
     const int n_cu = ctx().info.n_cu > 0 ? ctx().info.n_cu : 256;
-    const Args a = {g.A, g.B, g.sA, g.sB, g.C, g.offsets, g.ldc, g.M, g.N, (int)i8_padded(g.K), g.E,
-                    (int)(g.dtype == C3_F32), n_cu};
-    const Model model(g, a.P, n_cu);
-    Launch launch = launch_rounds<4, 2>;
-    double least = model.quarters({11.2, 1.03, 1.55, 0, 0});
-    auto consider = [&](double t, Launch l) {
-        if (t < least) {
-            least = t;
-            launch = l;
-        }
-    };
-    consider(model.quarters({7.4, 0.85, 1.69, 0, 0}), launch_rounds<2, 4>);
-    consider(model.tiles(128, 128, 2, {3.6, 0.475, 0.79, 0.93, 1.03}), launch_tile<2, 1, 2, 4>);
-    consider(model.tiles(128, 128, 1, {4.27, 0.34, 0.54, 0, 0}), launch_tile<2, 1, 4, 4>);
-    consider(model.tiles(128, 64, 1, {4.4, 0.24, 0.34, 0, 0}), launch_tile<2, 1, 4, 2>);
-    consider(model.tiles(64, 64, 2, {3.95, 0.11, 0.17, 0.42, 0.42}), launch_tile<1, 1, 4, 2>);
-    consider(model.tiles(64, 32, 2, {3.5, 0.1, 0.135, 0.3, 0.33}), launch_tile<1, 1, 4, 1>);
-    if (g.M <= 256 * (int64_t)model.used) {
-        consider(model.rows(16, 1, 1), launch_rows<16, 1, 1>);
-        consider(model.rows(16, 1, 2), launch_rows<16, 1, 2>);
-        consider(model.rows(16, 1, 4), launch_rows<16, 1, 4>);
-        consider(model.rows(16, 1, 8), launch_rows<16, 1, 8>);
-        consider(model.rows(32, 2, 1), launch_rows<32, 2, 1>);
-        consider(model.rows(32, 2, 2), launch_rows<32, 2, 2>);
-        consider(model.rows(32, 2, 4), launch_rows<32, 2, 4>);
-        consider(model.rows(32, 2, 8), launch_rows<32, 2, 8>);
-    }
+    const bool f32 = g.dtype == C3_F32;
+    const Args a = {g.A, g.B, g.sA, g.sB, g.C, g.offsets, g.ldc, g.M, g.N, (int)i8_padded(g.K), g.E, (int)f32, n_cu};
+    const Launch launch = kLaunch[i8::choose({g.M, g.N, a.P, g.E, g.offsets != nullptr, f32 ? 4 : 2}, n_cu)];
     if (!launch(g, a, stream) && !launch_rounds<4, 2>(g, a, stream))
         return fail(C3_E_INVALID, "int8 product: too many tiles");
     C3_HIP_TRY(hipGetLastError());
