@@ -47,7 +47,7 @@ class ExpertLayer:
         self.S = S
         self.up, self.down = Int8(E * F, D, dev).quantise(up), Int8(E * D, F, dev).quantise(down)
         whole = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)  # noqa: E731
-        # rows of no expert are left as they were: zeros
+        # rows of no expert are left as they were (zeros, or an earlier step's); no result comes from them
         half = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
         self.idx, self.weights = whole(T, self.k), torch.empty(T, self.k, device=dev)
         self.order, self.offsets, self.pos = whole(S), whole(E + 1), whole(S)
@@ -81,7 +81,8 @@ class ExpertLayer:
         return dz, dlogits
 
     def tokens_gradient(self, dx_rows):
-        """The sort's gradient: bf16 dx [T][D] from gradients dx_rows [S][D] of the sorted rows."""
+        """The sort's gradient: bf16 dx [T][D] from gradients dx_rows [S][D] of the sorted rows, which a
+        training program has from backward's dz by way of the experts' weights."""
         dx = torch.empty_like(self.y)
         c3.c3_combine(dx_rows, c3.C3_BF16, self.T, self.k, self.D, self.D, self.pos, None, dx, self.D,
                       torch.cuda.current_stream())
@@ -111,8 +112,9 @@ def main(T=8, E=32, D=4096, F=2048, k=4):
     torch.cuda.synchronize()
     print(f"{T} tokens, {E} experts of {D} x {F}, {k} each: {(time.perf_counter() - start) / n * 1e6:.1f} us a step")
     dz, dlogits = layer.backward(logits, randn(T, D).bfloat16())
+    # the experts' weights are quantised and have no gradient here: dz stands in for the sorted rows' own
     print("gradients: rows", tuple(dz.shape), "router", tuple(dlogits.shape),
-          "tokens", tuple(layer.tokens_gradient(dz).shape))
+          "and, as shapes go, rows brought back to tokens", tuple(layer.tokens_gradient(dz).shape))
     torch.cuda.synchronize()
 
 
