@@ -51,7 +51,7 @@ def rows_written(order, n):
 
 # T, k, cols: the first of each list are below the size from which tokens are gone through, the others above
 SORTS = [(40, 3, 72, 0), (40, 3, 72, 1), (5000, 4, 1032, 0), (2500, 6, 1101, 0), (4000, 4, 600, 1), (9000, 5, 257, 1),
-         (1700, 4, 3001, 0), (700, 8, 3001, 0), (90000, 8, 24, 0), (9000, 1, 8000, 0)]
+         (1700, 4, 3001, 0), (700, 8, 3001, 0), (90000, 8, 24, 0), (9000, 1, 8000, 0), (300000, 8, 8, 0), (1100000, 3, 4, 1)]
 QUANTISED = [(40, 3, 300, 0), (40, 3, 300, 1), (10000, 7, 100, 0), (5000, 3, 1032, 0), (1500, 2, 5000, 1), (300, 3, 17000, 0),
              (9000, 5, 200, 1)]
 
