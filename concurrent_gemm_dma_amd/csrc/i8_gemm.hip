@@ -209,16 +209,18 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // experts x 14336x4096 872 us against 890), and with 8, of which one scales and stores while another
 // still multiplies (8192x28672x512 239 us against 270). 128x128 comes with 8 only: 21.2 us against 25.5
 // on 1024x4096x4096, 13.3 against 14.9 on 2000x2000x2000. 64x32 for long K and too
-// few of 64x64: 128x4096x14336 29 us against 35, 64x8192x8192 19.9 and 22.7 (a CU takes in 50-60 GB/s
-// then; neither eight stages in LDS nor a whole stage's fragments in registers made it more).
+// few of 64x64: 128x4096x14336 29 us against 35, 64x8192x8192 19.9 and 22.7. What bounds products of few
+// tiles is open: on 128x8192x8192 and 1024x4096x4096 the matrix pipe is busy 13 and 37% of the cycles, LDS 14
+// and 31%, waves wait 75 and 44%, and neither eight stages in LDS nor a whole stage's fragments in registers
+// made them faster.
 //
 // Tiles of one XCD go through K in step, since they share rows of A and B in its L2; each XCD starts
 // an eighth of K further on (sums of integers have no order), so that not all ask the same memory
 // channels: 8192x28672x8192 in tiles of 128 1755 us against 1938, of 256 1471 against 1491; 1024 rows of
 // 8 experts x 8192x8192 108 against 132. Any further apart, the L2 is lost: 3025 and 1566.
 //
-// 8192x28672x8192 1.35-1.47 ms (2.6-2.8 POPS; hipBLASLt 1.90): matrix pipe busy 80% of the cycles at
-// 1.3-1.5 GHz under the power limit, at which matrix instructions alone, operands in registers and
+// 8192x28672x8192 1.35-1.49 ms (2.6-2.8 POPS; hipBLASLt 1.68-1.90): matrix pipe busy 79% of the cycles at
+// 1.5 GHz under the power limit, at which matrix instructions alone, operands in registers and
 // random, reach 3.6 POPS (4.95 on zeros). A tile's start and end cost a CU 9-11 us of 256x256 (half of
 // it scaling and storing 64 K sums, half first loads), which short K shows. One workgroup a CU that fetched
 // the next tile's first stages before storing gained nothing: its stores then held up the loads.
