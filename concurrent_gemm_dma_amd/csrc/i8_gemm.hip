@@ -219,7 +219,7 @@ __global__ __launch_bounds__(64 * W) void i8_gemm_rows(const Args g) {
 // channels: 8192x28672x8192 in tiles of 128 1755 us against 1938, of 256 1471 against 1491; 1024 rows of
 // 8 experts x 8192x8192 108 against 132. Any further apart, the L2 is lost: 3025 and 1566.
 //
-// 8192x28672x8192 1.35-1.49 ms (2.6-2.8 POPS; hipBLASLt 1.68-1.90): matrix pipe busy 79% of the cycles at
+// 8192x28672x8192 1.35-1.51 ms by card and codes (2.5-2.8 POPS; hipBLASLt 1.68-1.90): matrix pipe busy 79% of the cycles at
 // 1.5 GHz under the power limit, at which matrix instructions alone, operands in registers and
 // random, reach 3.6 POPS (4.95 on zeros). A tile's start and end cost a CU 9-11 us of 256x256 (half of
 // it scaling and storing 64 K sums, half first loads), which short K shows. One workgroup a CU that fetched
