@@ -10,7 +10,7 @@ from test_gpu_sort import CANARY, Rows, dev, routing, sync, values
 
 pytestmark = pytest.mark.gpu
 
-E = 8
+E = 64
 KINDS = ["dropped", "twice", "one slot", "both", "behind the end"]
 
 
@@ -51,9 +51,10 @@ def rows_written(order, n):
 
 # T, k, cols: the first of each list are below the size from which tokens are gone through, the others above
 SORTS = [(40, 3, 72, 0), (40, 3, 72, 1), (5000, 4, 1032, 0), (2500, 6, 1101, 0), (4000, 4, 600, 1), (9000, 5, 257, 1),
-         (1700, 4, 3001, 0), (700, 8, 3001, 0), (90000, 8, 24, 0), (9000, 1, 8000, 0), (300000, 8, 8, 0), (1100000, 3, 4, 1)]
+         (1700, 4, 3001, 0), (700, 8, 3001, 0), (90000, 8, 24, 0), (9000, 1, 8000, 0), (300000, 8, 8, 0), (1100000, 3, 4, 1),
+         (700, 40, 520, 0), (320, 37, 2400, 0)]
 QUANTISED = [(40, 3, 300, 0), (40, 3, 300, 1), (10000, 7, 100, 0), (5000, 3, 1032, 0), (1500, 2, 5000, 1), (300, 3, 17000, 0),
-             (9000, 5, 200, 1)]
+             (9000, 5, 200, 1), (2000, 40, 100, 0), (400, 17, 1100, 1)]
 
 
 @pytest.mark.parametrize("kind", KINDS)
